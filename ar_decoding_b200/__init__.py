@@ -16,9 +16,19 @@ libtidar.so is missing or a call fails, an exception is raised.
 maps ``free_pages`` [capacity] and ``free_count`` [1] (int32): the stack of free
 page ids that ``reserve`` pops the next step's draft pages from, after pushing
 the ids the commit released.
+
+Around the step, for a cache held in 4 bits (``kv4_cache``; the same table and
+lengths) and for the layer's products:
+
+    t = build_tables(table, ctx_lens, new_lens, pool, page_size=64, num_pages=N, max_rows=T)
+    kv4_append(cache4, k_rows, v_rows, t["slots"])
+    out, lse = step_attn_kv4(q, k_blk, v_blk, cache4, k, max_prefix_len=P)
+    commit_kv4(cache4, accept_count, k, head_dim=D, max_prefix_len=P)
+    y = linear_fused(x, w, bias=b, activation="silu", residual=r)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -36,6 +46,7 @@ PATH_AUTO, PATH_SIMT, PATH_TC05, PATH_DEC, PATH_PAIR = 0, 1, 2, 3, 4
 DEVERR_BAD_PAGE, DEVERR_BAD_LEN, DEVERR_BAD_COUNT, DEVERR_TIMEOUT, DEVERR_LAYOUT = 1, 2, 4, 8, 16
 DEVERR_POOL = 32
 PART_STEP_KEYS, PART_APPEND = 1, 2
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _PATHS = {"auto": PATH_AUTO, "simt": PATH_SIMT, "tc05": PATH_TC05, "dec": PATH_DEC,
           "pair": PATH_PAIR}
 
@@ -57,6 +68,19 @@ class StepDesc(ctypes.Structure):
 class PagePool(ctypes.Structure):
     _fields_ = [("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p),
                 ("capacity", ctypes.c_int32)]
+
+
+class TablesDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32)]
+
+
+class Kv4Desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("k_row_stride", ctypes.c_int64), ("v_row_stride", ctypes.c_int64)]
 
 
 class Sampling(ctypes.Structure):
@@ -136,6 +160,26 @@ def lib():
         L.tidar_layer_step_workspace_bytes.restype = S
         L.tidar_layer_step.argtypes = [P, P, I, P, P, P, ctypes.c_float, P, P, P, S, P]
         L.tidar_layer_step.restype = ctypes.c_int
+        L.tidar_build_tables.argtypes = [P] * 11
+        L.tidar_build_tables.restype = ctypes.c_int
+        L.tidar_kv4_page_bytes.argtypes = [I, I]
+        L.tidar_kv4_page_bytes.restype = S
+        L.tidar_kv4_append.argtypes = [P] * 7
+        L.tidar_kv4_append.restype = ctypes.c_int
+        L.tidar_kv4_gather.argtypes = [P] * 7
+        L.tidar_kv4_gather.restype = ctypes.c_int
+        L.tidar_step_attn_kv4_workspace_bytes.argtypes = [P]
+        L.tidar_step_attn_kv4_workspace_bytes.restype = S
+        L.tidar_step_attn_kv4.argtypes = [P, P, P, P, P, I, P, P, P, S, P]
+        L.tidar_step_attn_kv4.restype = ctypes.c_int
+        L.tidar_step_attn_kv4_plan.argtypes = [P, P, P, P]
+        L.tidar_step_attn_kv4_plan.restype = ctypes.c_int
+        L.tidar_commit_kv4.argtypes = [P, P, P, P, P, P]
+        L.tidar_commit_kv4.restype = ctypes.c_int
+        L.tidar_linear_fused_workspace_bytes.argtypes = [I, I, I]
+        L.tidar_linear_fused_workspace_bytes.restype = S
+        L.tidar_linear_fused.argtypes = [I, I, I, ctypes.c_int, P, P, P, ctypes.c_int, P, P, P, S, P]
+        L.tidar_linear_fused.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -636,18 +680,25 @@ def verify_commit(logits, drafts, cache, k, mode="greedy", *, max_prefix_len, dr
     return outputs, released, num_released
 
 
-def reserve(cache, pool, k, *, max_prefix_len, returned=None, num_returned=None, stream=None):
+def reserve(cache, pool, k, *, max_prefix_len, returned=None, num_returned=None, head_dim=None,
+            stream=None):
     """Pages for the draft rows of the next step, popped from a device stack.
 
     ``pool`` maps ``free_pages`` [capacity] int32 (ids [0, free_count) free)
     and ``free_count`` [1] int32, both device tensors.  ``returned`` /
     ``num_returned`` (e.g. what ``commit`` returned) are pushed first.
-    Updates ``cache["page_table"]`` and the pool in place."""
+    Updates ``cache["page_table"]`` and the pool in place.  ``head_dim`` is
+    needed (for the page size) with a cache held in 4 bits."""
     kp = cache["k_pages"]
     B = cache["seq_lens"].shape[0]
-    Hkv, ps, D = kp.shape[1], kp.shape[2], kp.shape[3]
+    if kp.dtype == torch.uint8:
+        if head_dim is None:
+            raise ValueError("head_dim is needed with a cache held in 4 bits")
+        Hkv, ps, D, dtype = kp.shape[1], _kv4_page_size(cache, head_dim, kp.device), head_dim, BF16
+    else:
+        Hkv, ps, D, dtype = kp.shape[1], kp.shape[2], kp.shape[3], _dtype_code(kp)
     desc = StepDesc(batch=B, num_q_heads=Hkv, num_kv_heads=Hkv, head_dim=D, k=k, page_size=ps,
-                    max_prefix_len=int(max_prefix_len), dtype=_dtype_code(kp), softmax_scale=0.0,
+                    max_prefix_len=int(max_prefix_len), dtype=dtype, softmax_scale=0.0,
                     path=PATH_AUTO)
     cdesc = make_cache_desc(cache, kp.device)
     fp, fc = pool["free_pages"], pool["free_count"]
@@ -663,6 +714,286 @@ def reserve(cache, pool, k, *, max_prefix_len, returned=None, num_returned=None,
     st = lib().tidar_reserve(ctypes.byref(desc), ctypes.byref(cdesc), ctypes.byref(p),
                              _ptr(returned), _ptr(num_returned), _stream_handle(stream))
     _check(st, "tidar_reserve")
+
+
+@contextlib.contextmanager
+def _launching(dev, stream):
+    """The handle of the stream a call on `dev` is queued on (`stream`, or the
+    current one of that device), with the device current.  What the call
+    allocates belongs to that stream, so it is not handed out again before the
+    call is done."""
+    if not isinstance(dev, torch.device) or dev.type != "cuda":
+        raise ValueError(f"the call's tensors are on {dev}, not on a CUDA device")
+    if stream is None:
+        if dev.index == torch.cuda.current_device():
+            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        else:
+            with torch.cuda.device(dev):
+                yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    else:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the call's tensors are on {dev}")
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _shaped(t, name, shape, dtype, dev):
+    _dev(t, name, dtype, dev)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} is {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def build_tables(page_table, ctx_lens, new_lens, pool, *, page_size, num_pages, max_rows, out=None,
+                 stream=None):
+    """Page table, slot map and positions of the rows that each sequence gets
+    (``new_lens`` on top of ``ctx_lens``), the missing pages popped from ``pool``.
+    Returns a dict of device tensors: ``page_table``, ``free_count``,
+    ``row_starts`` [B+1], ``slots`` [max_rows] int64 and ``positions`` [max_rows].
+    ``out`` may bring any of them (``page_table`` and ``pool["free_count"]``
+    themselves for an update in place); the inputs are otherwise left alone."""
+    _dev(page_table, "page_table", torch.int32)
+    dev = page_table.device
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table is {tuple(page_table.shape)}, expected [B][max_pages]")
+    B, width = page_table.shape
+    _shaped(ctx_lens, "ctx_lens", (B,), torch.int32, dev)
+    _shaped(new_lens, "new_lens", (B,), torch.int32, dev)
+    fp, fc = pool["free_pages"], pool["free_count"]
+    _shaped(fc, "free_count", (1,), torch.int32, dev)
+    _dev(fp, "free_pages", torch.int32, dev)
+    max_rows = int(max_rows)
+    if max_rows < 0:
+        raise ValueError(f"max_rows is {max_rows}")
+    res = dict(out) if out else {}
+    with _launching(dev, stream) as s:
+        for name, shape, dtype in (("page_table", (B, width), torch.int32), ("free_count", (1,), torch.int32),
+                                   ("row_starts", (B + 1,), torch.int32), ("slots", (max_rows,), torch.int64),
+                                   ("positions", (max_rows,), torch.int32)):
+            if name in res:
+                _shaped(res[name], name, shape, dtype, dev)
+            else:
+                res[name] = torch.empty(shape, dtype=dtype, device=dev)
+        d = TablesDesc(batch=B, page_size=int(page_size), num_pages=int(num_pages), max_pages_per_seq=width,
+                       max_rows=max_rows)
+        p = PagePool(free_pages=fp.data_ptr() or None, free_count=fc.data_ptr(), capacity=fp.numel())
+        st = lib().tidar_build_tables(ctypes.byref(d), _ptr(page_table), _ptr(ctx_lens), _ptr(new_lens),
+                                      ctypes.byref(p), _ptr(res["page_table"]), _ptr(res["free_count"]),
+                                      _ptr(res["row_starts"]), _ptr(res["slots"]), _ptr(res["positions"]), s)
+    _check(st, "tidar_build_tables")
+    return res
+
+
+def kv4_page_bytes(page_size: int, head_dim: int) -> int:
+    """Bytes of one page of one KV head in the 4-bit cache."""
+    n = int(lib().tidar_kv4_page_bytes(int(page_size), int(head_dim)))
+    if not n:
+        raise ValueError(f"no 4-bit pages of {page_size} rows of {head_dim} dims")
+    return n
+
+
+def kv4_cache(num_pages, num_kv_heads, page_size, head_dim, page_table, seq_lens):
+    """A cache mapping with zeroed 4-bit pages on the table's device."""
+    shape = (num_pages, num_kv_heads, kv4_page_bytes(page_size, head_dim))
+    return dict(k_pages=torch.zeros(shape, dtype=torch.uint8, device=page_table.device),
+                v_pages=torch.zeros(shape, dtype=torch.uint8, device=page_table.device),
+                page_table=page_table, seq_lens=seq_lens)
+
+
+def _kv4_page_size(cache, head_dim, dev):
+    """page_size of a 4-bit cache whose rows are head_dim long."""
+    kp, vp = cache["k_pages"], cache["v_pages"]
+    _dev(kp, "k_pages", torch.uint8, dev)
+    _dev(vp, "v_pages", torch.uint8, dev)
+    if kp.dim() != 3 or vp.shape != kp.shape:
+        raise ValueError(f"k_pages {tuple(kp.shape)} and v_pages {tuple(vp.shape)} must both be "
+                         "[num_pages][Hkv][page_bytes]")
+    row = head_dim // 2 + head_dim // 16
+    if head_dim not in (64, 128) or kp.shape[2] % row or kp.shape[2] // row not in (16, 32, 64, 128):
+        raise ValueError(f"pages of {kp.shape[2]} bytes do not hold 16, 32, 64 or 128 rows of {head_dim} dims "
+                         "(64 or 128) in 4 bits")
+    return kp.shape[2] // row
+
+
+def _row_stride(t, name, dtype, dev):
+    """Elements between the rows of t [T][Hkv][D], whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name} must be a CUDA tensor [rows][Hkv][D]")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors are on {dev}")
+    T, H, D = t.shape
+    if t.is_contiguous() or T == 0:
+        return H * D
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D) or (T > 1 and t.stride(0) < H * D):
+        raise ValueError(f"{name} must hold whole rows of [Hkv][D] (strides {t.stride()})")
+    return t.stride(0) if T > 1 else H * D
+
+
+def _kv4_desc(cache, k, v, slots):
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("rows must be CUDA tensors [rows][Hkv][D]")
+    dev = k.device
+    d = Kv4Desc(rows=k.shape[0], num_kv_heads=k.shape[1], head_dim=k.shape[2], dtype=_dtype_code(k),
+                k_row_stride=_row_stride(k, "k_rows", k.dtype, dev),
+                v_row_stride=_row_stride(v, "v_rows", k.dtype, dev))
+    if v.shape != k.shape:
+        raise ValueError(f"k_rows {tuple(k.shape)} and v_rows {tuple(v.shape)} disagree")
+    d.page_size = _kv4_page_size(cache, k.shape[2], dev)
+    d.num_pages = cache["k_pages"].shape[0]
+    if cache["k_pages"].shape[1] != k.shape[1]:
+        raise ValueError(f"the cache holds {cache['k_pages'].shape[1]} heads, the rows {k.shape[1]}")
+    _shaped(slots, "slots", (k.shape[0],), torch.int64, dev)
+    return d, dev
+
+
+def kv4_append(cache, k_rows, v_rows, slots, *, stream=None):
+    """Quantise rows [T][Hkv][D] (row strides allowed: a slice of a projection's
+    output) and store them at ``slots`` [T] int64; a negative slot skips its row."""
+    d, dev = _kv4_desc(cache, k_rows, v_rows, slots)
+    with _launching(dev, stream) as s:
+        st = lib().tidar_kv4_append(ctypes.byref(d), _ptr(cache["k_pages"]), _ptr(cache["v_pages"]), _ptr(k_rows),
+                                    _ptr(v_rows), _ptr(slots), s)
+    _check(st, "tidar_kv4_append")
+
+
+def kv4_gather(cache, slots, *, head_dim=None, dtype=torch.bfloat16, out=None, stream=None):
+    """The values stored at ``slots`` [T]: (k_rows, v_rows) [T][Hkv][D].  Rows
+    whose slot is negative are left as they were (zeros when allocated here)."""
+    _dev(slots, "slots", torch.int64)
+    dev = slots.device
+    with _launching(dev, stream) as s:
+        if out is None:
+            if head_dim is None:
+                raise ValueError("head_dim is needed when out is not given")
+            if dtype not in (torch.float32, torch.bfloat16):
+                raise ValueError(f"unsupported dtype {dtype}")
+            shape = (slots.numel(), cache["k_pages"].shape[1], head_dim)
+            out = (torch.zeros(shape, dtype=dtype, device=dev), torch.zeros(shape, dtype=dtype, device=dev))
+        k, v = out
+        d, dev2 = _kv4_desc(cache, k, v, slots)
+        st = lib().tidar_kv4_gather(ctypes.byref(d), _ptr(cache["k_pages"]), _ptr(cache["v_pages"]), _ptr(slots),
+                                    _ptr(k), _ptr(v), s)
+    _check(st, "tidar_kv4_gather")
+    return k, v
+
+
+def step_attn_kv4_desc(q, k_blk, cache, k, max_prefix_len, scale=0.0, path="auto") -> StepDesc:
+    B, R, Hq, D = q.shape
+    return StepDesc(batch=B, num_q_heads=Hq, num_kv_heads=k_blk.shape[2], head_dim=D, k=k,
+                    page_size=_kv4_page_size(cache, D, q.device), max_prefix_len=int(max_prefix_len),
+                    dtype=_dtype_code(q), softmax_scale=float(scale), path=_PATHS[path])
+
+
+def kv4_plan(desc: StepDesc) -> tuple[int, int, int]:
+    """``plan_full`` of step_attn_kv4."""
+    path, splits, merge = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
+    _check(lib().tidar_step_attn_kv4_plan(ctypes.byref(desc), ctypes.byref(path), ctypes.byref(splits),
+                                          ctypes.byref(merge)), "tidar_step_attn_kv4_plan")
+    return path.value, splits.value, merge.value
+
+
+def step_attn_kv4_workspace_bytes(desc: StepDesc) -> int:
+    return int(lib().tidar_step_attn_kv4_workspace_bytes(ctypes.byref(desc)))
+
+
+def step_attn_kv4(q, k_blk, v_blk, cache, k, *, max_prefix_len, step_keys=True, append=True, scale=0.0,
+                  path="auto", out=None, lse=None, want_lse=True, workspace=None, stream=None):
+    """Three-zone step attention over a cache held in 4 bits.  ``append`` stores
+    the draft rows too (quantised); ``step_keys=False`` attends the cache alone.
+    Returns (out, lse)."""
+    _dev(q, "q")
+    dev = q.device
+    if q.dim() != 4 or not isinstance(k_blk, torch.Tensor) or k_blk.dim() != 4:
+        raise ValueError("q must be [B][R][Hq][D], k_blk and v_blk [B][R][Hkv][D]")
+    B, R, Hq, D = q.shape
+    H = k_blk.shape[2]
+    if R != (1 if k == 0 else k + k * k):
+        raise ValueError(f"q has {R} rows per sequence, k = {k} needs {1 if k == 0 else k + k * k}")
+    _shaped(k_blk, "k_blk", (B, R, H, D), q.dtype, dev)
+    _shaped(v_blk, "v_blk", (B, R, H, D), q.dtype, dev)
+    desc = step_attn_kv4_desc(q, k_blk, cache, k, max_prefix_len, scale, path)
+    cdesc = make_cache_desc(cache, dev)
+    if cache["k_pages"].shape[1] != H:
+        raise ValueError(f"the cache holds {cache['k_pages'].shape[1]} heads, k_blk {H}")
+    if cache["page_table"].shape[0] != B or cache["seq_lens"].shape[0] != B:
+        raise ValueError(f"the cache's table and lengths must be of {B} sequences")
+    flags = (PART_STEP_KEYS if step_keys else 0) | (PART_APPEND if append else 0)
+    with _launching(dev, stream) as s:
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty((B, R, Hq), dtype=torch.float32, device=dev)
+        _shaped(out, "out", q.shape, q.dtype, dev)
+        if lse is not None:
+            _shaped(lse, "lse", (B, R, Hq), torch.float32, dev)
+        ws, wbytes = _scratch(step_attn_kv4_workspace_bytes(desc), workspace, dev)
+        st = lib().tidar_step_attn_kv4(ctypes.byref(desc), ctypes.byref(cdesc), _ptr(q), _ptr(k_blk), _ptr(v_blk),
+                                       flags, _ptr(out), _ptr(lse), _ptr(ws), wbytes, s)
+    _check(st, "tidar_step_attn_kv4")
+    return out, lse
+
+
+def commit_kv4(cache, accept_count, k, *, head_dim, max_prefix_len, released=None, num_released=None,
+               stream=None):
+    """``commit`` for a cache held in 4 bits.  Returns (released, num_released)."""
+    kp = cache["k_pages"]
+    _dev(kp, "k_pages", torch.uint8)
+    dev = kp.device
+    ps = _kv4_page_size(cache, head_dim, dev)
+    B, H, n = cache["seq_lens"].shape[0], kp.shape[1], max(k, 1)
+    desc = StepDesc(batch=B, num_q_heads=H, num_kv_heads=H, head_dim=head_dim, k=k, page_size=ps,
+                    max_prefix_len=int(max_prefix_len), dtype=BF16, softmax_scale=0.0, path=PATH_AUTO)
+    cdesc = make_cache_desc(cache, dev)
+    _shaped(accept_count, "accept_count", (B,), torch.int32, dev)
+    cap = B * ((n + ps - 1) // ps + 1)
+    with _launching(dev, stream) as s:
+        if released is None:
+            released = torch.empty(cap, dtype=torch.int32, device=dev)
+        if num_released is None:
+            num_released = torch.empty(1, dtype=torch.int32, device=dev)
+        _shaped(released, "released", (cap,), torch.int32, dev)
+        _shaped(num_released, "num_released", (1,), torch.int32, dev)
+        st = lib().tidar_commit_kv4(ctypes.byref(desc), ctypes.byref(cdesc), _ptr(accept_count), _ptr(released),
+                                    _ptr(num_released), s)
+    _check(st, "tidar_commit_kv4")
+    return released, num_released
+
+
+def linear_fused_workspace_bytes(rows: int, out_features: int, in_features: int) -> int:
+    return int(lib().tidar_linear_fused_workspace_bytes(int(rows), int(out_features), int(in_features)))
+
+
+def linear_fused(x, w, *, bias=None, activation="none", residual=None, out=None, workspace=None, stream=None):
+    """y = activation(x w^T + bias) + residual (bf16; x [..., in], w [out][in])
+    on the tensor cores, rounded once.  ``activation``: none, relu, gelu (erf),
+    gelu_tanh or silu.  ``residual`` has y's shape and may be ``out`` itself."""
+    _dev(x, "x", torch.bfloat16)
+    dev = x.device
+    _dev(w, "w", torch.bfloat16, dev)
+    if w.dim() != 2 or x.dim() < 1 or x.shape[-1] != w.shape[1]:
+        raise ValueError(f"x is {tuple(x.shape)}, w {tuple(w.shape)}: x must be [..., in], w [out][in]")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation is {activation!r}, expected one of {sorted(ACTIVATIONS)}")
+    N, K = w.shape
+    shape = (*x.shape[:-1], N)
+    rows = 1
+    for n in x.shape[:-1]:
+        rows *= n
+    if bias is not None:
+        _shaped(bias, "bias", (N,), torch.bfloat16, dev)
+    if residual is not None:
+        _shaped(residual, "residual", shape, torch.bfloat16, dev)
+    with _launching(dev, stream) as s:
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        else:
+            _shaped(out, "out", shape, torch.bfloat16, dev)
+        ws, wbytes = _scratch(linear_fused_workspace_bytes(rows, N, K), workspace, dev)
+        st = lib().tidar_linear_fused(rows, N, K, BF16, _ptr(x), _ptr(w), _ptr(bias), ACTIVATIONS[activation],
+                                      _ptr(residual), _ptr(out), _ptr(ws), wbytes, s)
+    _check(st, "tidar_linear_fused")
+    return out
 
 
 DEBUG_STARVE_ATTENTION_LOADS, DEBUG_FORCE_SPLIT_PARTIALS = 1, 2

@@ -95,13 +95,14 @@ tidar_status check_cache(const tidar_step_desc* d, const tidar_kv_cache* c) {
 
 constexpr bool kTc05Built = true;
 
-bool tc05_supported(const tidar_step_desc* d) {
+bool tc05_supported(const tidar_step_desc* d, bool kv4 = false) {
+  if (kv4) return false;
   return kTc05Built && d->dtype == TIDAR_BF16 && d->head_dim == 128 && d->page_size == 64;
 }
 
 // Warp-MMA decode kernel: at most 16 packed query rows per KV head.
-bool dec_supported(const tidar_step_desc* d) {
-  return tc05_supported(d) &&
+bool dec_supported(const tidar_step_desc* d, bool kv4 = false) {
+  return tc05_supported(d, kv4) &&
          (long long)tidar::rows_per_seq(d->k) * (d->num_q_heads / d->num_kv_heads) <= 16;
 }
 
@@ -143,7 +144,7 @@ int max_step_windows(const tidar_step_desc* d, int path) {
 // Key ranges are multiples of 128 keys (64 on the decode path).  SIMT: aim for
 // ~2 waves of 4-warp CTAs.  TC05 / PAIR / DEC: one CTA per SM and per (b, kv
 // head, query tile or pair of tiles, split), split count from a cost model.
-Plan make_plan(const tidar_step_desc* d, int path) {
+Plan make_plan(const tidar_step_desc* d, int path, bool kv4 = false) {
   Plan p;
   p.path = path;
   const int R = tidar::rows_per_seq(d->k);
@@ -237,12 +238,39 @@ Plan make_plan(const tidar_step_desc* d, int path) {
   return p;
 }
 
-int choose_path(const tidar_step_desc* d) {
+int choose_path(const tidar_step_desc* d, bool kv4 = false) {
   if (d->path == TIDAR_PATH_SIMT) return 1;
   if (d->path == TIDAR_PATH_TC05) return 2;
   if (d->path == TIDAR_PATH_DEC) return 3;
   if (d->path == TIDAR_PATH_PAIR) return 4;
-  return dec_supported(d) ? 3 : (tc05_supported(d) ? 2 : 1);
+  return dec_supported(d, kv4) ? 3 : (tc05_supported(d, kv4) ? 2 : 1);
+}
+
+// Whether the family `path` takes this call.
+bool path_supported(const tidar_step_desc* d, int path, bool kv4) {
+  if (path == 4) return !kv4 && tc05_supported(d);
+  return path == 1 || (path == 2 && tc05_supported(d, kv4)) || (path == 3 && dec_supported(d, kv4));
+}
+
+size_t step_workspace_bytes(const tidar_step_desc* d, bool kv4) {
+  if (check_desc(d) != TIDAR_OK) return 0;
+  const Plan p = make_plan(d, choose_path(d, kv4), kv4);
+  if (p.nsplit <= 1 || p.cluster_merge) return 0;     // one split, or merged in the kernel
+  const size_t rows = (size_t)d->batch * tidar::rows_per_seq(d->k) * d->num_q_heads;
+  return align256((size_t)p.nsplit * rows * d->head_dim * sizeof(float)) +
+         align256((size_t)p.nsplit * rows * sizeof(float));
+}
+
+tidar_status step_plan(const tidar_step_desc* d, bool kv4, int32_t* path, int32_t* splits, int32_t* merge) {
+  const tidar_status st = check_desc(d);
+  if (st != TIDAR_OK) return st;
+  const int pth = choose_path(d, kv4);
+  if (!path_supported(d, pth, kv4)) return TIDAR_ERR_UNSUPPORTED;
+  const Plan p = make_plan(d, pth, kv4);
+  if (path) *path = p.path;
+  if (splits) *splits = p.nsplit;
+  if (merge) *merge = p.nsplit <= 1 ? 0 : (p.cluster_merge ? 1 : 2);
+  return TIDAR_OK;
 }
 
 }  // namespace
@@ -265,27 +293,16 @@ const char* tidar_last_cuda_error(void) { return g_cuda_msg; }
 
 tidar_status tidar_step_attn_plan(const tidar_step_desc* desc, int32_t* path, int32_t* splits,
                                   int32_t* merge) {
-  tidar_status st = check_desc(desc);
-  if (st != TIDAR_OK) return st;
-  const int pth = choose_path(desc);
-  if ((pth == 2 || pth == 4) && !tc05_supported(desc)) return TIDAR_ERR_UNSUPPORTED;
-  if (pth == 3 && !dec_supported(desc)) return TIDAR_ERR_UNSUPPORTED;
-  const Plan p = make_plan(desc, pth);
-  if (path) *path = p.path;
-  if (splits) *splits = p.nsplit;
-  if (merge) *merge = p.nsplit <= 1 ? 0 : (p.cluster_merge ? 1 : 2);
-  return TIDAR_OK;
+  return step_plan(desc, false, path, splits, merge);
 }
 
-size_t tidar_step_attn_workspace_bytes(const tidar_step_desc* d) {
-  if (check_desc(d) != TIDAR_OK) return 0;
-  const int pth = choose_path(d);
-  const Plan p = make_plan(d, pth);
-  if (p.nsplit <= 1 || p.cluster_merge) return 0;     // one split, or merged in the kernel
-  const size_t rows = (size_t)d->batch * tidar::rows_per_seq(d->k) * d->num_q_heads;
-  return align256((size_t)p.nsplit * rows * d->head_dim * sizeof(float)) +
-         align256((size_t)p.nsplit * rows * sizeof(float));
+tidar_status tidar_step_attn_kv4_plan(const tidar_step_desc* desc, int32_t* path, int32_t* splits, int32_t* merge) {
+  return step_plan(desc, true, path, splits, merge);
 }
+
+size_t tidar_step_attn_workspace_bytes(const tidar_step_desc* d) { return step_workspace_bytes(d, false); }
+
+size_t tidar_step_attn_kv4_workspace_bytes(const tidar_step_desc* d) { return step_workspace_bytes(d, true); }
 
 }  // extern "C"
 
@@ -296,7 +313,7 @@ namespace {
 tidar_status step_attn_impl(const tidar_step_desc* d, const tidar_kv_cache* c, const void* q,
                             const void* k_blk, const void* v_blk, void* out, float* lse_out,
                             void* workspace, size_t workspace_bytes, tidar_stream_t stream, int step_keys,
-                            int append) {
+                            int append, bool kv4 = false) {
   tidar_status st = check_desc(d);
   if (st != TIDAR_OK) return st;
   if (d->batch == 0) return TIDAR_OK;
@@ -304,11 +321,11 @@ tidar_status step_attn_impl(const tidar_step_desc* d, const tidar_kv_cache* c, c
   if (!q || !k_blk || !v_blk || !out) return TIDAR_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_blk) || !aligned16(v_blk) || !aligned16(out))
     return TIDAR_ERR_INVALID_ARG;
-  const int pth = choose_path(d);
-  if ((pth == 2 || pth == 4) && !tc05_supported(d)) return TIDAR_ERR_UNSUPPORTED;
-  if (pth == 3 && !dec_supported(d)) return TIDAR_ERR_UNSUPPORTED;
-  const Plan p = make_plan(d, pth);
-  const size_t need = tidar_step_attn_workspace_bytes(d);
+  const int pth = choose_path(d, kv4);
+  if (!path_supported(d, pth, kv4)) return TIDAR_ERR_UNSUPPORTED;
+  if (kv4 && (long long)d->batch * d->num_kv_heads > 65535) return TIDAR_ERR_UNSUPPORTED;   // the launch grid
+  const Plan p = make_plan(d, pth, kv4);
+  const size_t need = step_workspace_bytes(d, kv4);
   if (workspace_bytes < need) return TIDAR_ERR_INVALID_ARG;
   if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
     return TIDAR_ERR_INVALID_ARG;
@@ -330,6 +347,7 @@ tidar_status step_attn_impl(const tidar_step_desc* d, const tidar_kv_cache* c, c
   a.scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / sqrtf((float)d->head_dim);
   a.step_keys = step_keys;
   a.append = append;
+  a.kv4 = kv4 ? 1 : 0;
   a.cluster_merge = p.cluster_merge ? 1 : 0;
   if (p.nsplit > 1 && !p.cluster_merge) {
     const size_t rows = (size_t)a.B * a.R * a.Hq;
@@ -372,6 +390,15 @@ tidar_status tidar_step_attn_part(const tidar_step_desc* d, const tidar_kv_cache
   if (!lse_out) return TIDAR_ERR_INVALID_ARG;
   return step_attn_impl(d, c, q, k_blk, v_blk, out, lse_out, workspace, workspace_bytes, stream,
                         (flags & TIDAR_PART_STEP_KEYS) ? 1 : 0, (flags & TIDAR_PART_APPEND) ? 1 : 0);
+}
+
+tidar_status tidar_step_attn_kv4(const tidar_step_desc* d, const tidar_kv_cache* c, const void* q, const void* k_blk,
+                                 const void* v_blk, int32_t flags, void* out, float* lse_out, void* workspace,
+                                 size_t workspace_bytes, tidar_stream_t stream) {
+  if (flags & ~(TIDAR_PART_STEP_KEYS | TIDAR_PART_APPEND)) return TIDAR_ERR_INVALID_ARG;
+  if (!(flags & TIDAR_PART_STEP_KEYS) && !lse_out) return TIDAR_ERR_INVALID_ARG;
+  return step_attn_impl(d, c, q, k_blk, v_blk, out, lse_out, workspace, workspace_bytes, stream,
+                        (flags & TIDAR_PART_STEP_KEYS) ? 1 : 0, (flags & TIDAR_PART_APPEND) ? 1 : 0, true);
 }
 
 tidar_status tidar_merge_attn(int32_t nparts, int64_t rows, int32_t head_dim, tidar_dtype dtype,
@@ -450,7 +477,8 @@ tidar_status verify_launch(int32_t batch, int32_t k, int32_t vocab, tidar_dtype 
 
 // Host checks of a commit and its launch arguments (nothing queued).
 tidar_status commit_prepare(const tidar_step_desc* d, const tidar_kv_cache* c, const int32_t* accept_count,
-                            int32_t* released_pages, int32_t* num_released, tidar::CommitArgs& a) {
+                            int32_t* released_pages, int32_t* num_released, tidar::CommitArgs& a,
+                            bool kv4 = false) {
   tidar_status st = check_desc(d);
   if (st != TIDAR_OK) return st;
   if (d->batch == 0) return TIDAR_OK;
@@ -465,6 +493,7 @@ tidar_status commit_prepare(const tidar_step_desc* d, const tidar_kv_cache* c, c
   a.k_pages = c->k_pages; a.v_pages = c->v_pages; a.page_table = c->page_table;
   a.seq_lens = c->seq_lens; a.accept_count = accept_count; a.released = released_pages;
   a.num_released = num_released; a.err = err;
+  a.kv4 = kv4 ? 1 : 0;
   return TIDAR_OK;
 }
 
@@ -582,6 +611,15 @@ tidar_status tidar_commit(const tidar_step_desc* d, const tidar_kv_cache* c,
   return TIDAR_OK;
 }
 
+tidar_status tidar_commit_kv4(const tidar_step_desc* d, const tidar_kv_cache* c, const int32_t* accept_count,
+                              int32_t* released_pages, int32_t* num_released, tidar_stream_t stream) {
+  tidar::CommitArgs a{};
+  const tidar_status st = commit_prepare(d, c, accept_count, released_pages, num_released, a, true);
+  if (st != TIDAR_OK || d->batch == 0) return st;
+  const cudaError_t e = tidar::launch_commit(a, nullptr, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TIDAR_OK : cuda_fail(e);
+}
+
 tidar_status tidar_verify_commit(const tidar_step_desc* d, const tidar_kv_cache* c, int32_t vocab,
                                  tidar_dtype dtype, tidar_accept_mode mode, const void* logits,
                                  const int32_t* drafts, const void* draft_logits, const float* uniforms,
@@ -668,6 +706,38 @@ tidar_status tidar_linear(int32_t rows, int32_t out_features, int32_t in_feature
   if (e == cudaErrorNotSupported) return TIDAR_ERR_UNSUPPORTED;
   if (e != cudaSuccess) return cuda_fail(e);
   return TIDAR_OK;
+}
+
+size_t tidar_linear_fused_workspace_bytes(int32_t rows, int32_t out_features, int32_t in_features) {
+  if (rows <= 0 || out_features <= 0 || in_features <= 0 || in_features % 8) return 0;
+  const tidar::LinearPlan p = tidar::plan_linear_any(rows, in_features, out_features);
+  return p.ok ? p.ws_bytes : 0;
+}
+
+tidar_status tidar_linear_fused(int32_t rows, int32_t out_features, int32_t in_features, tidar_dtype dtype,
+                                const void* x, const void* w, const void* bias, tidar_activation activation,
+                                const void* residual, void* y, void* workspace, size_t workspace_bytes,
+                                tidar_stream_t stream) {
+  if (rows < 0 || out_features <= 0 || in_features <= 0) return TIDAR_ERR_INVALID_ARG;
+  if (activation < TIDAR_ACT_NONE || activation > TIDAR_ACT_SILU) return TIDAR_ERR_INVALID_ARG;
+  if (dtype != TIDAR_BF16 || in_features % 8) return TIDAR_ERR_UNSUPPORTED;
+  if (rows == 0) return TIDAR_OK;
+  if (!x || !w || !y || !aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(bias) || !aligned16(residual))
+    return TIDAR_ERR_INVALID_ARG;
+  const tidar::LinearPlan p = tidar::plan_linear_any(rows, in_features, out_features);
+  if (!p.ok) return TIDAR_ERR_UNSUPPORTED;
+  if (workspace_bytes < p.ws_bytes || (p.ws_bytes && !workspace) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return TIDAR_ERR_INVALID_ARG;
+  tidar::LinearArgs a{};
+  a.T = rows; a.K = in_features; a.N = out_features; a.mode = 2;
+  a.x = x; a.w = w; a.y = y; a.ws = workspace;
+  a.bias = bias; a.residual = residual; a.act = activation;
+  const tidar_status st = error_word(&a.err);
+  if (st != TIDAR_OK) return st;
+  const cudaError_t e = tidar::launch_linear(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return TIDAR_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? TIDAR_OK : cuda_fail(e);
 }
 
 size_t tidar_qkv_rope_workspace_bytes(const tidar_step_desc* d, int32_t d_model) {

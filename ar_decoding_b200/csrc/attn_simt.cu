@@ -12,10 +12,14 @@
 // the head dimension; keys are visited in order with an online softmax in
 // fp32 (accurate expf).  Split-KV: blockIdx.y selects a contiguous key range;
 // the last split also takes the step keys.
+//
+// KV4: the prefix comes from the 4-bit cache (kv4.cuh); a lane's slice of a key
+// is dequantised as it is loaded, the rest is the same.
 #include <math.h>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "kv4.cuh"
 
 namespace tidar {
 
@@ -23,7 +27,7 @@ namespace {
 
 constexpr int kWarps = 4;
 
-template <typename T, int D>
+template <typename T, int D, bool KV4>
 __global__ void __launch_bounds__(kWarps * 32) attn_simt_kernel(AttnArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -98,7 +102,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_simt_kernel(AttnArgs a) {
   // prefix keys of this split
   const int k0 = split * a.keys_per_split;
   const int k1 = min(P, k0 + a.keys_per_split);
-  const T* kpages = static_cast<const T*>(a.k_pages);
+  const T* kpages = static_cast<const T*>(a.k_pages);   // KV4: bytes, see below
   const T* vpages = static_cast<const T*>(a.v_pages);
   const int32_t* table = a.page_table + (size_t)b * a.max_pages;
   bool bad_page = false;
@@ -114,9 +118,15 @@ __global__ void __launch_bounds__(kWarps * 32) attn_simt_kernel(AttnArgs a) {
         if (page < 0 || page >= a.num_pages) {
           bad_page = true;
         } else {
-          const size_t off = ((size_t)(page * a.Hkv + g) * a.page_size + key % a.page_size) * D + lane * VPL;
-          load_vec<T, VPL>(kpages + off, kv[u]);
-          load_vec<T, VPL>(vpages + off, vv[u]);
+          if constexpr (KV4) {
+            const size_t off = ((size_t)page * a.Hkv + g) * kv4_page_bytes(a.page_size, D);
+            kv4_load_slice<D>(static_cast<const uint8_t*>(a.k_pages) + off, true, a.page_size, key % a.page_size, lane, kv[u]);
+            kv4_load_slice<D>(static_cast<const uint8_t*>(a.v_pages) + off, false, a.page_size, key % a.page_size, lane, vv[u]);
+          } else {
+            const size_t off = ((size_t)(page * a.Hkv + g) * a.page_size + key % a.page_size) * D + lane * VPL;
+            load_vec<T, VPL>(kpages + off, kv[u]);
+            load_vec<T, VPL>(vpages + off, vv[u]);
+          }
           ok[u] = true;
         }
       }
@@ -165,7 +175,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_simt_kernel(AttnArgs a) {
 
 // Merge the split partials (weights exp(lse_s - max)) and, in the blocks past
 // the merge, copy the draft rows' K/V into the cache at P_b .. P_b+n-1.
-template <typename T, int D>
+template <typename T, int D, bool KV4>
 __global__ void __launch_bounds__(kWarps * 32) finalize_kernel(AttnArgs a, int merge_blocks) {
   pdl_wait();
   pdl_trigger();
@@ -230,6 +240,26 @@ __global__ void __launch_bounds__(kWarps * 32) finalize_kernel(AttnArgs a, int m
   const int page = a.page_table[(size_t)b * a.max_pages + pos / a.page_size];
   if (page < 0 || page >= a.num_pages) {
     if (threadIdx.x == 0) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
+    return;
+  }
+  if constexpr (KV4) {
+    // four lanes per (K or V, head), whole warps (kv4_store_quad)
+    const int units = 2 * a.Hkv, y = (int)threadIdx.x & 3;
+    for (int u0 = ((int)threadIdx.x >> 5) * 8; u0 < units; u0 += kWarps * 8) {
+      const int u = u0 + (((int)threadIdx.x & 31) >> 2);
+      const bool live = u < units;
+      const bool is_key = u < a.Hkv;
+      const int g = live ? (is_key ? u : u - a.Hkv) : 0;
+      const T* src = static_cast<const T*>(is_key ? a.k_blk : a.v_blk) + ((size_t)(b * a.R + r) * a.Hkv + g) * D;
+      float x[D / 32][8];
+#pragma unroll
+      for (int G = 0; G < D / 32; ++G)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[G][e] = to_f32(src[32 * G + 8 * y + e]);
+      uint8_t* base = static_cast<uint8_t*>(const_cast<void*>(is_key ? a.k_pages : a.v_pages)) +
+                      ((size_t)page * a.Hkv + g) * kv4_page_bytes(a.page_size, D);
+      kv4_store_quad<D>(x, is_key, base, a.page_size, pos % a.page_size, live);
+    }
     return;
   }
   constexpr int kVec = 16 / sizeof(T);     // elements per 16-byte chunk
@@ -299,7 +329,8 @@ template <typename T, int D>
 cudaError_t launch_simt_t(const AttnArgs& a, cudaStream_t s) {
   const int M = a.R * a.G;
   dim3 grid((M + kWarps - 1) / kWarps, a.nsplit, a.B * a.Hkv);
-  return launch_pdl(attn_simt_kernel<T, D>, grid, kWarps * 32, 0, s, a);
+  if (a.kv4) return launch_pdl(attn_simt_kernel<T, D, true>, grid, kWarps * 32, 0, s, a);
+  return launch_pdl(attn_simt_kernel<T, D, false>, grid, kWarps * 32, 0, s, a);
 }
 
 template <typename T, int D>
@@ -308,7 +339,8 @@ cudaError_t launch_finalize_t(const AttnArgs& a, cudaStream_t s) {
   const int merge_blocks = a.nsplit > 1 ? (int)((rows + kWarps - 1) / kWarps) : 0;
   const int blocks = merge_blocks + (a.append ? a.B * a.n : 0);
   if (blocks == 0) return cudaSuccess;
-  return launch_pdl(finalize_kernel<T, D>, dim3(blocks), kWarps * 32, 0, s, a, merge_blocks);
+  if (a.kv4) return launch_pdl(finalize_kernel<T, D, true>, dim3(blocks), kWarps * 32, 0, s, a, merge_blocks);
+  return launch_pdl(finalize_kernel<T, D, false>, dim3(blocks), kWarps * 32, 0, s, a, merge_blocks);
 }
 
 }  // namespace

@@ -29,6 +29,7 @@
 #include "accept.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include "kv4.cuh"
 
 namespace tidar {
 
@@ -250,7 +251,30 @@ __global__ void __launch_bounds__(kCThreads) commit_cluster_kernel(CommitArgs a,
   const int t0 = spread ? rank * kCThreads + (int)threadIdx.x : (int)threadIdx.x;
   const int tstep = spread ? C * kCThreads : kCThreads;
   const size_t row_bytes = (size_t)a.D * a.elem_bytes;
-  if (tstep % cols == 0) {
+  if (a.kv4) {
+    // 4-bit pages: one thread per (row, K or V, head), its codes and scales
+    const int units = 2 * a.Hkv;
+    const size_t page_bytes = kv4_page_bytes(ps, a.D);
+    const int cb = kv4_code_bytes(a.D), sbytes = kv4_scale_bytes(a.D);
+    for (int i = 0; i < nscrub; ++i) {
+      const SeqRec r = spread ? s_all[i] : s_rec[i];
+      const int* pg = spread ? s_allpg + i * npm : s_pg + i * npm;
+      if (r.cnt < 0) continue;
+      const int p0 = r.P / ps;
+      for (int t = t0; t < (a.n - r.c) * units; t += tstep) {
+        const int rr = t / units, u = t - rr * units;
+        const int which = u >= a.Hkv, g = u - which * a.Hkv;
+        const int pos = r.P + r.c + rr;
+        const int row = pos % ps;
+        char* base = static_cast<char*>(which ? a.v_pages : a.k_pages) +
+                     ((size_t)pg[pos / ps - p0] * a.Hkv + g) * page_bytes;
+        uint4* code = reinterpret_cast<uint4*>(base + (size_t)row * cb);
+        for (int e = 0; e < cb / 16; ++e) code[e] = make_uint4(0, 0, 0, 0);
+        uint32_t* scale = reinterpret_cast<uint32_t*>(base + (size_t)ps * cb + (size_t)row * sbytes);
+        for (int e = 0; e < sbytes / 4; ++e) scale[e] = 0;
+      }
+    }
+  } else if (tstep % cols == 0) {
     // Each thread keeps one 16-byte column (K or V, head, piece) and walks
     // the rejected rows tstep / cols apart: the column's decomposition is
     // computed once, each store costs a page lookup.
@@ -329,7 +353,8 @@ cudaError_t launch_commit_t(const CommitArgs& a, const GreedyAcceptArgs& f, cuda
   // them faster than a cluster barrier takes), up to the largest cluster: with
   // a small batch the CTAs share the zeroing, and a small cluster finds its
   // SMs free while the previous kernel's CTAs still hold most of the others.
-  const size_t scrub = (size_t)a.B * a.n * 2 * a.Hkv * a.D * a.elem_bytes;
+  const size_t row_bytes = a.kv4 ? (size_t)(kv4_code_bytes(a.D) + kv4_scale_bytes(a.D)) : (size_t)a.D * a.elem_bytes;
+  const size_t scrub = (size_t)a.B * a.n * 2 * a.Hkv * row_bytes;
   const int C = scrub <= (32u << 10)
                     ? 1
                     : (int)std::min<size_t>(cluster_limit(commit_cluster_kernel<kFused>, kCThreads, limit_cache),

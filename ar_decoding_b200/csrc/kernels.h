@@ -28,6 +28,7 @@ struct AttnArgs {
   float scale;           // softmax scale (natural-log domain)
   int step_keys;         // 1: the last split also attends the step keys (the zone mask); 0: prefix only
   int append;            // 1: write the draft rows' K/V into the cache
+  int kv4;               // 1: k_pages / v_pages hold the 4-bit pages of kv4.cuh
   int cluster_merge;     // nsplit > 1: the splits of a tile are one cluster and merge in the kernel
                          // (part_o unused); 0: partials in part_o / part_lse, a finalize launch merges
 };
@@ -132,6 +133,7 @@ struct GreedyAcceptArgs {
 
 struct CommitArgs {
   int B, Hkv, D, k, n, page_size, elem_bytes, max_pages, num_pages;
+  int kv4;                       // 1: 4-bit pages (kv4.cuh); elem_bytes unused
   void* k_pages;
   void* v_pages;
   int32_t* page_table;
@@ -164,7 +166,8 @@ cudaError_t launch_reserve(const ReserveArgs& a, cudaStream_t s);
 
 // Projections on either side of the step attention (tcgen05 GEMM, weights
 // [N][K] bf16 as the A operand, token rows [T][K] bf16 as B).  mode 0: y
-// [T][N] bf16.  mode 1: the query/key/value projection of the R rows of each
+// [T][N] bf16.  mode 2: y = act(x w^T + bias) + residual, any N, K a multiple
+// of 8.  mode 1: the query/key/value projection of the R rows of each
 // sequence (T = B R, N = (Hq + 2 Hkv) 128), rotary embedding of queries and
 // keys at their zone positions, outputs q / k_blk / v_blk.
 struct LinearArgs {
@@ -178,6 +181,9 @@ struct LinearArgs {
   const int32_t* seq_lens;
   int Hq, Hkv, R, k, max_prefix;
   double log2_base;
+  const void* bias;      // mode 2: [N] bf16 or null
+  const void* residual;  // mode 2: [T][N] bf16 or null (may be y itself)
+  int act;               // mode 2: tidar_activation
   unsigned int* err;
   void* ws;          // plan.ws_bytes of device scratch (split partials), 256-byte aligned
 };
@@ -192,6 +198,9 @@ struct LinearPlan {
 // take (K not a multiple of 64, N not a multiple of 128).  The split count
 // depends on the current device's cluster occupancy (queried once).
 LinearPlan plan_linear(int T, int K, int N);
+// The same for any N and K: the last feature tile and the last 64-deep slice
+// of the reduction are partly outside the tensors, where TMA reads zeros.
+LinearPlan plan_linear_any(int T, int K, int N);
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 
 }  // namespace tidar

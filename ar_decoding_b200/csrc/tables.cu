@@ -1,0 +1,297 @@
+// tables.cu -- page tables and slot maps built on the device from request
+// lengths.
+//
+// A batch is admitted (whole prompts) or stepped (a few rows a sequence) by
+// the lengths alone: sequence b holds ctx_b rows and gets new_b more, packed
+// one sequence after the other into a token buffer.  With ps rows to a page,
+//   start_b   = new_0 + .. + new_{b-1}
+//   entries   ceil(ctx_b / ps) .. ceil((ctx_b + new_b) / ps) - 1 of its table
+//             row that are -1 pop the stack of free pages, in (b, entry) order
+//   slot(start_b + i) = table[b][(ctx_b + i) / ps] * ps + (ctx_b + i) % ps
+// Integer work of a few bytes a row (8 of slot, 4 of position), so what bounds
+// it is latency: the prefix sums over the sequences, then one table read and
+// one store a row.
+//
+// Two launches.  tables_kernel: one thread-block cluster; CTA r owns a
+// contiguous range of sequences (one warp per sequence), counts the entries
+// that need a page, scans rows and counts over its range, reads the other
+// CTAs' totals over distributed shared memory, and writes its table rows.
+// slots_kernel: the whole device, one thread per pair of token rows (one
+// 16-byte store of two slots), the row's sequence found by bisection of the
+// starts, which sit in shared memory up to kStartsMax sequences.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace tidar {
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+constexpr int kTThreads = 512;
+constexpr int kTWarps = kTThreads / 32;
+constexpr int kTMaxCluster = 8;           // portable
+constexpr int kTablesMaxBatch = 65536;
+constexpr int kSThreads = 256;
+constexpr int kStartsMax = 8192;
+
+struct TablesArgs {
+  int B, ps, num_pages, max_pages, max_rows, capacity;
+  const int32_t* table_in;
+  const int32_t* ctx;
+  const int32_t* newl;
+  const int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* table_out;
+  int32_t* count_out;
+  int32_t* starts;
+  int64_t* slots;
+  int32_t* positions;
+  unsigned int* err;
+};
+
+// One owned sequence: rows it adds (0 when its lengths are invalid), the pages
+// it needs (0 when it is skipped), both then replaced by exclusive sums.
+struct TabRec {
+  long long rows, need;
+  int ok;
+};
+
+__global__ void __launch_bounds__(kTThreads) tables_kernel(TablesArgs a, int per) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  extern __shared__ __align__(16) unsigned char s_raw[];
+  TabRec* rec = reinterpret_cast<TabRec*>(s_raw);
+  __shared__ long long s_rows, s_need, w_rows[kTWarps], w_need[kTWarps];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int b0 = rank * per, nown = max(0, min(a.B, b0 + per) - b0);
+  const int ps = a.ps;
+  pdl_wait();
+  pdl_trigger();
+
+  // 1. validate and count, one warp per sequence
+  for (int i = wid; i < nown; i += kTWarps) {
+    const int b = b0 + i;
+    const int c = a.ctx[b], m = a.newl[b];
+    const bool len_ok = c >= 0 && m >= 0 && (long long)c + m <= (long long)a.max_pages * ps;
+    if (!len_ok && lane == 0) raise_error(a.err, TIDAR_DEVERR_BAD_LEN);
+    int need = 0;
+    bool bad = false;
+    if (len_ok && m > 0) {
+      const int32_t* row = a.table_in + (size_t)b * a.max_pages;
+      const int first = (int)(((long long)c + ps - 1) / ps), last = (int)(((long long)c + m + ps - 1) / ps);
+      for (int e0 = c / ps; e0 < last; e0 += 128) {
+        int id[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int e = e0 + 32 * u + lane;
+          id[u] = e < last ? row[e] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int e = e0 + 32 * u + lane;
+          const bool in = e < last, want = in && e >= first && id[u] == -1;
+          bad = bad || (in && !want && (id[u] < 0 || id[u] >= a.num_pages));
+          need += __popc(__ballot_sync(0xffffffffu, want));
+        }
+      }
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) {
+      if (bad) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
+      TabRec r;
+      r.rows = m > 0 ? m : 0;
+      r.ok = len_ok && !bad;
+      r.need = r.ok ? need : 0;
+      rec[i] = r;
+    }
+  }
+  __syncthreads();
+  // 2. exclusive sums over this CTA's range: a contiguous run per thread, then
+  //    over the threads
+  {
+    const int run = (nown + kTThreads - 1) / kTThreads;
+    const int i0 = min(nown, (int)threadIdx.x * run), i1 = min(nown, i0 + run);
+    long long rows = 0, need = 0;
+    for (int i = i0; i < i1; ++i) rows += rec[i].rows, need += rec[i].need;
+    long long xr = rows, xn = need;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long yr = __shfl_up_sync(0xffffffffu, xr, o), yn = __shfl_up_sync(0xffffffffu, xn, o);
+      if (lane >= o) xr += yr, xn += yn;
+    }
+    if (lane == 31) w_rows[wid] = xr, w_need[wid] = xn;
+    __syncthreads();
+    long long br = 0, bn = 0;
+    for (int w = 0; w < wid; ++w) br += w_rows[w], bn += w_need[w];
+    xr += br - rows;
+    xn += bn - need;
+    for (int i = i0; i < i1; ++i) {
+      const long long r = rec[i].rows, q = rec[i].need;
+      rec[i].rows = xr;
+      rec[i].need = xn;
+      xr += r;
+      xn += q;
+    }
+    if (threadIdx.x == kTThreads - 1) s_rows = xr, s_need = xn;
+  }
+  // 3. bases across the cluster
+  cl.sync();
+  long long base_r = 0, all_r = 0, base_n = 0, all_n = 0;
+  for (int r = 0; r < C; ++r) {
+    const long long x = *cl.map_shared_rank(&s_rows, r), y = *cl.map_shared_rank(&s_need, r);
+    if (r < rank) base_r += x, base_n += y;
+    all_r += x;
+    all_n += y;
+  }
+  const int count = *a.free_count;
+  const bool pool_ok = count >= 0 && count <= a.capacity && all_n <= count;
+  const bool ok = pool_ok && all_r <= a.max_rows;
+  cl.sync();                     // no CTA leaves, or rewrites the count, while a peer reads
+  if (rank == 0 && threadIdx.x == 0) {
+    if (!pool_ok) raise_error(a.err, TIDAR_DEVERR_POOL);
+    if (all_r > a.max_rows) raise_error(a.err, TIDAR_DEVERR_BAD_COUNT);
+    *a.count_out = ok ? count - (int)all_n : count;
+    a.starts[a.B] = (int32_t)min(all_r, (long long)a.max_rows);
+  }
+  // 4. the table rows and the starts (a start past the token buffer is its end)
+  for (int i = wid; i < nown; i += kTWarps) {
+    const int b = b0 + i;
+    const TabRec r = rec[i];
+    if (lane == 0) a.starts[b] = (int32_t)min(base_r + r.rows, (long long)a.max_rows);
+    const int c = a.ctx[b], m = a.newl[b];
+    const int32_t* src = a.table_in + (size_t)b * a.max_pages;
+    int32_t* dst = a.table_out + (size_t)b * a.max_pages;
+    const bool fill = ok && r.ok && m > 0;
+    const int first = fill ? (int)(((long long)c + ps - 1) / ps) : a.max_pages;
+    const int last = fill ? (int)(((long long)c + m + ps - 1) / ps) : 0;
+    long long pop = base_n + r.need;              // pages popped before this entry
+    for (int e0 = 0; e0 < a.max_pages; e0 += 128) {
+      int id[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int e = e0 + 32 * u + lane;
+        id[u] = e < a.max_pages ? src[e] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int e = e0 + 32 * u + lane;
+        const bool want = e >= first && e < last && id[u] == -1;
+        const unsigned m32 = __ballot_sync(0xffffffffu, want);
+        if (want) id[u] = a.free_pages[count - 1 - (pop + __popc(m32 & ((1u << lane) - 1u)))];
+        pop += __popc(m32);
+        if (e < a.max_pages && (want || dst != src)) dst[e] = id[u];
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kSThreads) slots_kernel(TablesArgs a) {
+  extern __shared__ __align__(16) unsigned char s_raw[];
+  int32_t* s_starts = reinterpret_cast<int32_t*>(s_raw);
+  const bool local = a.B <= kStartsMax;
+  pdl_wait();
+  pdl_trigger();
+  if (local) {
+    for (int i = threadIdx.x; i <= a.B; i += kSThreads) s_starts[i] = a.starts[i];
+    __syncthreads();
+  }
+  const int32_t* starts = local ? s_starts : a.starts;
+  const int total = starts[a.B];
+  bool bad = false;
+  for (long long r0 = 2 * ((long long)blockIdx.x * kSThreads + threadIdx.x); r0 < a.max_rows;
+       r0 += 2LL * gridDim.x * kSThreads) {
+    long long slot[2] = {-1, -1};
+    int pos[2] = {-1, -1};
+    int b = 0;
+    if (r0 < total) {
+      // the last sequence that starts at or before the row (empty ones before it share its start)
+      int lo = 0, hi = a.B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (starts[mid] <= r0) lo = mid;
+        else hi = mid - 1;
+      }
+      b = lo;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const long long r = r0 + u;
+      if (r >= total) continue;
+      while (b + 1 < a.B && starts[b + 1] <= r) ++b;
+      const int c = a.ctx[b];
+      const long long p = (long long)c + (r - starts[b]);
+      if (c < 0 || p >= (long long)a.max_pages * a.ps) continue;       // reported by tables_kernel
+      pos[u] = (int)p;
+      const int page = a.table_out[(size_t)b * a.max_pages + p / a.ps];
+      if (page < 0 || page >= a.num_pages) bad = true;
+      else slot[u] = (long long)page * a.ps + p % a.ps;
+    }
+    if (r0 + 1 < a.max_rows) {
+      *reinterpret_cast<longlong2*>(a.slots + r0) = make_longlong2(slot[0], slot[1]);
+      if (a.positions) *reinterpret_cast<int2*>(a.positions + r0) = make_int2(pos[0], pos[1]);
+    } else {
+      a.slots[r0] = slot[0];
+      if (a.positions) a.positions[r0] = pos[0];
+    }
+  }
+  if (bad) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
+}
+
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+}  // namespace tidar
+
+extern "C" tidar_status tidar_build_tables(const tidar_tables_desc* d, const int32_t* page_table,
+                                           const int32_t* ctx_lens, const int32_t* new_lens,
+                                           const tidar_page_pool* pool, int32_t* page_table_out,
+                                           int32_t* free_count_out, int32_t* row_starts, int64_t* slots,
+                                           int32_t* positions, tidar_stream_t stream) {
+  using namespace tidar;
+  if (!d) return TIDAR_ERR_INVALID_ARG;
+  if (d->batch < 0 || d->max_pages_per_seq <= 0 || d->num_pages <= 0 || d->max_rows < 0 || d->page_size <= 0)
+    return TIDAR_ERR_INVALID_ARG;
+  if (d->page_size != 16 && d->page_size != 32 && d->page_size != 64 && d->page_size != 128)
+    return TIDAR_ERR_UNSUPPORTED;
+  if (d->batch > kTablesMaxBatch || (long long)d->max_pages_per_seq * d->page_size > 0x7fffffffLL)
+    return TIDAR_ERR_UNSUPPORTED;
+  if (d->batch == 0) return TIDAR_OK;
+  if (!page_table || !ctx_lens || !new_lens || !page_table_out || !free_count_out || !row_starts ||
+      (d->max_rows > 0 && !slots))
+    return TIDAR_ERR_INVALID_ARG;
+  if (!pool || !pool->free_count || pool->capacity < 0 || (pool->capacity > 0 && !pool->free_pages))
+    return TIDAR_ERR_INVALID_ARG;
+  if (!aligned(slots, 16) || !aligned(positions, 8)) return TIDAR_ERR_INVALID_ARG;
+  TablesArgs a{};
+  a.B = d->batch; a.ps = d->page_size; a.num_pages = d->num_pages; a.max_pages = d->max_pages_per_seq;
+  a.max_rows = d->max_rows; a.capacity = pool->capacity;
+  a.table_in = page_table; a.ctx = ctx_lens; a.newl = new_lens; a.free_pages = pool->free_pages;
+  a.free_count = pool->free_count; a.table_out = page_table_out; a.count_out = free_count_out;
+  a.starts = row_starts; a.slots = slots; a.positions = positions;
+  const tidar_status st = error_word_status(&a.err);
+  if (st != TIDAR_OK) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // one warp per sequence, up to the portable cluster
+  const int C = std::min(kTMaxCluster, (a.B + kTWarps - 1) / kTWarps);
+  const int per = (a.B + C - 1) / C;
+  const size_t smem = (size_t)per * sizeof(TabRec);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024) {
+    e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  e = launch_cluster(tables_kernel, C, 1, kTThreads, smem, s, a, per);
+  if (e != cudaSuccess) return cuda_status(e);
+  if (a.max_rows > 0) {
+    const long long pairs = ((long long)a.max_rows + 1) / 2;
+    const int grid = (int)std::min<long long>((pairs + kSThreads - 1) / kSThreads, 148 * 8);
+    e = launch_pdl(slots_kernel, dim3(grid), kSThreads, a.B <= kStartsMax ? (size_t)(a.B + 1) * 4 : 0, s, a);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  return TIDAR_OK;
+}

@@ -466,6 +466,113 @@ tidar_status tidar_reserve(const tidar_step_desc* desc, const tidar_kv_cache* ca
                            const int32_t* num_returned, tidar_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Page tables and slot maps from request lengths (no counterpart on the pages:
+ * the admission of requests around the step).  Sequence b holds ctx_lens[b]
+ * rows and gets new_lens[b] more; the new rows of all sequences are packed one
+ * sequence after the other into a token buffer of max_rows rows.
+ *   row_starts[b] = new_0 + .. + new_{b-1}, row_starts[B] = their total
+ *   entries ceil(ctx/ps) .. ceil((ctx+new)/ps)-1 of table row b: kept if a
+ *     valid page, popped from the pool's stack if -1, in (b, entry) order (the
+ *     t-th takes free_pages[count-1-t]); an entry that also holds rows below
+ *     ctx must be valid.  Every other entry is copied as it is.
+ *   slots[row_starts[b] + i] = page_table_out[b][(ctx+i)/ps] * ps + (ctx+i)%ps
+ *     (-1 where that entry is not a valid page), positions[..] = ctx + i;
+ *     both -1 for rows past the total, up to max_rows.
+ * page_table_out may be page_table and free_count_out may be pool->free_count
+ * (in place); the pool's ids are not written.  Any other overlap of an output
+ * is not allowed.
+ * Device errors: BAD_LEN (ctx < 0, new < 0 or ctx + new > max_pages_per_seq *
+ * ps: the sequence gets no pages; a negative new counts as no rows), BAD_PAGE
+ * (an entry it needs is neither valid nor -1, or -1 below ctx: the sequence
+ * gets no pages; or a popped id is no page), POOL (too few free pages or a bad
+ * count) and BAD_COUNT (more than max_rows rows; row_starts then stop at
+ * max_rows): with these two no sequence gets pages and the count stays.
+ * TIDAR_ERR_UNSUPPORTED: page_size not 16, 32, 64 or 128, batch > 65536,
+ * max_pages_per_seq * page_size >= 2^31.  batch 0: nothing is written.
+ *   page_table, page_table_out [B][max_pages_per_seq]; ctx_lens, new_lens [B];
+ *   free_count_out [1]; row_starts [B+1] int32; slots [max_rows] int64, 16-byte
+ *   aligned; positions [max_rows] int32, 8-byte aligned, or NULL.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t batch;             /* B */
+  int32_t page_size;         /* 16, 32, 64 or 128 */
+  int32_t num_pages;         /* valid page ids are [0, num_pages) */
+  int32_t max_pages_per_seq; /* width of the table */
+  int32_t max_rows;          /* rows of the token buffer */
+} tidar_tables_desc;
+
+tidar_status tidar_build_tables(const tidar_tables_desc* desc, const int32_t* page_table,
+                                const int32_t* ctx_lens, const int32_t* new_lens,
+                                const tidar_page_pool* pool, int32_t* page_table_out,
+                                int32_t* free_count_out, int32_t* row_starts, int64_t* slots,
+                                int32_t* positions, tidar_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The cache held in 4 bits (no counterpart on the pages; a smaller form of
+ * their exact KV cache for long prefixes).  A tidar_kv_cache whose k_pages and
+ * v_pages are [num_pages][Hkv][page_bytes] bytes, page_bytes =
+ * tidar_kv4_page_bytes(page_size, head_dim) = page_size * (D/2 + D/16); table
+ * and lengths as in any cache.  A row is D/32 groups of 32 dims: a scale s =
+ * max|x|/7 rounded to 5 significant bits and codes c = x/s rounded to the
+ * nearest integer (ties to even), |c| <= 7; a dim stands for c * s, which is
+ * exact in bf16.  A group whose largest magnitude is below 2^-120 stands for
+ * zeros; one that holds 2^126 or more, an infinity or a NaN stands for NaNs.
+ * Zeroed bytes stand for zeros.
+ * Bytes of a page of one head: page_size rows of D/2 code bytes, then page_size
+ * rows of D/32 bf16 scales.  With n = D/32 and dim d = 32G + 8y + 2i + h (y, i
+ * < 4, h < 2) the code is nibble i (lowest first, two's complement) of the
+ * row's little-endian 16-bit unit y*2n + 2G + h (keys) or y*2n + h*n + G
+ * (values).
+ *
+ * tidar_kv4_append: stores rows k_rows, v_rows [rows][Hkv][D] (rows k_row_stride
+ *   / v_row_stride elements apart, 0 = contiguous; multiples of 16 bytes) at
+ *   slots[row] = page * page_size + row in page, as tidar_build_tables writes
+ *   them.  A negative slot skips its row, one past the cache does so with
+ *   BAD_PAGE.  The slots of a call must differ (else the content of a slot
+ *   named twice is unspecified).
+ * tidar_kv4_gather: the values of the rows at `slots`, exact in either dtype;
+ *   rows whose slot is negative or past the cache are left as they were.
+ * tidar_step_attn_kv4: tidar_step_attn_part over such a cache: flags as there
+ *   (TIDAR_PART_STEP_KEYS: the step keys, read from k_blk / v_blk as they are;
+ *   TIDAR_PART_APPEND: the draft rows are quantised and stored); lse_out may be
+ *   NULL with STEP_KEYS.  desc->dtype is that of q, k_blk, v_blk and out.
+ *   Paths: AUTO or TIDAR_PATH_SIMT for every shape; workspace as
+ *   tidar_step_attn's, sized by tidar_step_attn_kv4_workspace_bytes.
+ *   TIDAR_ERR_UNSUPPORTED when batch * num_kv_heads > 65535.
+ * tidar_commit_kv4: tidar_commit over such a cache (rejected rows are zeroed).
+ * tidar_reserve and tidar_build_tables only touch the table and serve both.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t rows;          /* >= 0 */
+  int32_t num_kv_heads;  /* Hkv */
+  int32_t head_dim;      /* D: 64 or 128 */
+  int32_t page_size;     /* 16, 32, 64 or 128 */
+  int32_t num_pages;
+  tidar_dtype dtype;     /* of the rows */
+  int64_t k_row_stride;  /* elements between rows; 0: Hkv * D */
+  int64_t v_row_stride;
+} tidar_kv4_desc;
+
+size_t tidar_kv4_page_bytes(int32_t page_size, int32_t head_dim);   /* 0: unsupported */
+tidar_status tidar_kv4_append(const tidar_kv4_desc* desc, void* k_pages, void* v_pages,
+                              const void* k_rows, const void* v_rows, const int64_t* slots,
+                              tidar_stream_t stream);
+tidar_status tidar_kv4_gather(const tidar_kv4_desc* desc, const void* k_pages, const void* v_pages,
+                              const int64_t* slots, void* k_rows, void* v_rows,
+                              tidar_stream_t stream);
+size_t tidar_step_attn_kv4_workspace_bytes(const tidar_step_desc* desc);
+tidar_status tidar_step_attn_kv4(const tidar_step_desc* desc, const tidar_kv_cache* cache,
+                                 const void* q, const void* k_blk, const void* v_blk,
+                                 int32_t flags, void* out, float* lse_out, void* workspace,
+                                 size_t workspace_bytes, tidar_stream_t stream);
+/* tidar_step_attn_plan for tidar_step_attn_kv4. */
+tidar_status tidar_step_attn_kv4_plan(const tidar_step_desc* desc, int32_t* path, int32_t* splits,
+                                      int32_t* merge);
+tidar_status tidar_commit_kv4(const tidar_step_desc* desc, const tidar_kv_cache* cache,
+                              const int32_t* accept_count, int32_t* released_pages,
+                              int32_t* num_released, tidar_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Layer-level step: the projections on either side of the step attention.
  * [MS] §2 (one forward pass of the model over the three zones); [EN] section
  * "為什麼 GPU 在 AR 推論時是閒置的" (each AR decode step reloads every weight,
@@ -519,6 +626,25 @@ size_t tidar_linear_workspace_bytes(int32_t rows, int32_t out_features, int32_t 
 tidar_status tidar_linear(int32_t rows, int32_t out_features, int32_t in_features,
                           tidar_dtype dtype, const void* x, const void* w, void* y,
                           void* workspace, size_t workspace_bytes, tidar_stream_t stream);
+/* tidar_linear_fused: y [rows][out_features] = act(x w^T + bias) + residual, in
+ * fp32 and rounded to bf16 once.  bias [out_features] and residual [rows]
+ * [out_features] are bf16 or NULL; residual may be y itself.  Any out_features;
+ * in_features a multiple of 8 (else TIDAR_ERR_UNSUPPORTED).  GELU is 0.5 v (1 +
+ * erf(v / sqrt 2)), GELU_TANH its tanh form, SILU v / (1 + exp(-v)).  Every
+ * pointer 16-byte aligned; workspace as tidar_linear's, sized by
+ * tidar_linear_fused_workspace_bytes. */
+typedef enum {
+  TIDAR_ACT_NONE = 0,
+  TIDAR_ACT_RELU = 1,
+  TIDAR_ACT_GELU = 2,
+  TIDAR_ACT_GELU_TANH = 3,
+  TIDAR_ACT_SILU = 4
+} tidar_activation;
+size_t tidar_linear_fused_workspace_bytes(int32_t rows, int32_t out_features, int32_t in_features);
+tidar_status tidar_linear_fused(int32_t rows, int32_t out_features, int32_t in_features,
+                                tidar_dtype dtype, const void* x, const void* w, const void* bias,
+                                tidar_activation activation, const void* residual, void* y,
+                                void* workspace, size_t workspace_bytes, tidar_stream_t stream);
 size_t tidar_qkv_rope_workspace_bytes(const tidar_step_desc* desc, int32_t d_model);
 tidar_status tidar_qkv_rope(const tidar_step_desc* desc, int32_t d_model, const void* x,
                             const void* w_qkv, const int32_t* seq_lens, float rope_base,

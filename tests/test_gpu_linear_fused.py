@@ -1,0 +1,132 @@
+"""tidar_linear_fused against act(x w^T + bias) + residual in 64 bits.
+
+Tolerance: the fp32 sum of K exact products is off by at most (K/16 + 16) 2^-23
+of sum |x||w| + |bias| (blocks of 16 products, then splits); every activation
+here has a slope of at most 1.13, its own fp32 evaluation adds 16 roundings of
+its argument's size; the result is rounded to bf16 once (2^-8 of itself)."""
+import math
+
+import pytest
+import torch
+
+import ar_decoding_b200 as tidar
+
+pytestmark = pytest.mark.gpu
+
+
+def reference(x, w, bias, act, res):
+    x, w = x.double(), w.double()
+    y = x @ w.t()
+    mag = x.abs() @ w.abs().t()
+    if bias is not None:
+        y, mag = y + bias.double(), mag + bias.double().abs()
+    s = y
+    if act == "relu":
+        s = y.clamp(min=0)
+    elif act == "gelu":
+        s = y * torch.special.ndtr(y)
+    elif act == "gelu_tanh":
+        s = y * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (y + 0.044715 * y ** 3))
+    elif act == "silu":
+        s = y * torch.sigmoid(y)
+    want = s if res is None else s + res.double()
+    tol = 1.13 * (x.shape[-1] / 16 + 16) * 2.0 ** -23 * mag + 16 * 2.0 ** -23 * (y.abs() + want.abs()) + 2.0 ** -8 * want.abs()
+    return want, tol + 2.0 ** -133
+
+
+def data(seed, T, N, K, bias=True, res=True, x_scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    bf = lambda t: t.to(torch.bfloat16)  # noqa: E731
+    return (bf(r(T, K) * x_scale), bf(r(N, K) / math.sqrt(K)), bf(r(N)) if bias else None, bf(r(T, N)) if res else None)
+
+
+def check(got, want, tol):
+    err = (got.double() - want).abs()
+    assert torch.isfinite(got).all() and (err <= tol).all(), float((err / tol).max())
+
+
+@pytest.mark.parametrize("act", sorted(tidar.ACTIVATIONS))
+@pytest.mark.parametrize("bias,res", [(False, False), (True, False), (False, True), (True, True)])
+def test_epilogues(act, bias, res):
+    x, w, b, r = data(1, 50, 200, 256, bias, res, x_scale=3.0)
+    y = tidar.linear_fused(x, w, bias=b, activation=act, residual=r)
+    check(y, *reference(x, w, b, act, r))
+    assert tidar.device_status() == (tidar.OK, 0)
+
+
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 77, 255, 256, 257, 272, 288, 289, 513, 1111])
+@pytest.mark.parametrize("N,K", [(1, 8), (7, 64), (127, 72), (128, 4096), (130, 1544), (1000, 520), (2049, 200)])
+def test_odd_sizes(T, N, K):
+    x, w, b, r = data(T * 7 + N, T, N, K)
+    check(tidar.linear_fused(x, w, bias=b, activation="silu", residual=r), *reference(x, w, b, "silu", r))
+
+
+@pytest.mark.parametrize("T,N,K", [(272, 4096, 4096), (2048, 2048, 1024), (300, 6000, 8192), (4096, 384, 640)])
+def test_large(T, N, K):
+    x, w, b, r = data(3, T, N, K)
+    check(tidar.linear_fused(x, w, bias=b, activation="gelu_tanh", residual=r), *reference(x, w, b, "gelu_tanh", r))
+
+
+def test_neighbouring_memory_is_left_alone():
+    for T, N, K in ((5, 7, 64), (130, 129, 200), (300, 136, 64)):
+        x, w, b, r = data(5, T, N, K)
+        flat = torch.full((T * N + 64,), 77.0, dtype=torch.bfloat16, device="cuda")
+        tidar.linear_fused(x, w, bias=b, residual=r, out=flat[:T * N].view(T, N))
+        assert (flat[T * N:] == 77).all()
+        check(flat[:T * N].view(T, N), *reference(x, w, b, "none", r))
+
+
+def test_plain_epilogue_is_the_linear_layer():
+    x, w, _, _ = data(9, 64, 256, 512)
+    assert torch.equal(tidar.linear_fused(x, w), tidar.linear(x, w))
+
+
+def test_residual_in_place_and_leading_dims():
+    x, w, b, r = data(11, 60, 256, 512)
+    want, tol = reference(x, w, b, "gelu", r)
+    h = r.clone().view(3, 20, 256)
+    y = tidar.linear_fused(x.view(3, 20, 512), w, bias=b, activation="gelu", residual=h, out=h)
+    assert y is h
+    check(h.view(60, 256), want, tol)
+    assert tidar.linear_fused(x[:0], w).shape == (0, 256)
+
+
+def test_extreme_values():
+    x, w, b, _ = data(13, 4, 64, 64)
+    big = torch.tensor([3e38, -3e38, float("inf"), float("nan")], dtype=torch.bfloat16, device="cuda")
+    b[:4] = big
+    for act in tidar.ACTIVATIONS:
+        y = tidar.linear_fused(x * 0, w, bias=b, activation=act).float()
+        assert torch.isnan(y[:, 3]).all()
+        assert torch.isposinf(y[:, 2]).all() and (y[:, 0] > 2.9e38).all()
+        assert (y[:, 1] == (float(b[1]) if act == "none" else 0)).all()
+
+
+def test_refusals():
+    x, w, b, r = data(15, 6, 64, 64)
+    for kw in (dict(bias=b[:8]), dict(residual=r[:2]), dict(activation="tanh"), dict(out=r.float()), dict(bias=b.float()),
+               dict(residual=r.t())):
+        with pytest.raises(ValueError):
+            tidar.linear_fused(x, w, **kw)
+    with pytest.raises(ValueError):
+        tidar.linear_fused(x, w[:, :32].contiguous())
+    with pytest.raises(tidar.TidarError):
+        tidar.linear_fused(x[:, :60].contiguous(), w[:, :60].contiguous())
+
+
+def test_two_streams_and_capture():
+    x, w, b, r = data(17, 272, 2048, 4096)
+    want = tidar.linear_fused(x, w, bias=b, activation="silu", residual=r)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        got.append(tidar.linear_fused(x, w, bias=b, activation="silu", residual=r, stream=s))
+    ws = torch.empty(max(256, tidar.linear_fused_workspace_bytes(272, 2048, 4096)), dtype=torch.uint8, device="cuda")
+    out, g = torch.zeros_like(want), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tidar.linear_fused(x, w, bias=b, activation="silu", residual=r, out=out, workspace=ws)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in got) and torch.equal(out, want)
