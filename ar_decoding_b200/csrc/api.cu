@@ -102,7 +102,7 @@ bool tc05_supported(const tidar_step_desc* d, bool kv4 = false) {
 
 // Warp-MMA decode kernel: at most 16 packed query rows per KV head.
 bool dec_supported(const tidar_step_desc* d, bool kv4 = false) {
-  return tc05_supported(d, kv4) &&
+  return (kv4 ? d->dtype == TIDAR_BF16 && d->head_dim == 128 : tc05_supported(d)) &&
          (long long)tidar::rows_per_seq(d->k) * (d->num_q_heads / d->num_kv_heads) <= 16;
 }
 
@@ -225,8 +225,9 @@ Plan make_plan(const tidar_step_desc* d, int path, bool kv4 = false) {
     if (cost_p < best) { best = cost_p; best_n = n; best_cluster = false; }
     if (p.nsplit > 1 && p.nsplit <= 16 && !g_force_partials) {
       const int resident = path == 2 ? tidar::tc05_resident_clusters(p.nsplit)
-                                     : (path == 4 ? tidar::pair_resident_clusters(p.nsplit)
-                                                  : tidar::dec_resident_clusters(p.nsplit, M));
+                                     : path == 4 ? tidar::pair_resident_clusters(p.nsplit)
+                           : kv4       ? tidar::kv4_dec_resident_clusters(p.nsplit, M)
+                                       : tidar::dec_resident_clusters(p.nsplit, M);
       if (resident > 0) {
         const double cost_c = (double)((units + resident - 1) / resident) * per + kClusterMergeBlocks;
         if (cost_c <= best) { best = cost_c; best_n = n; best_cluster = true; }   // ties: on chip
@@ -357,7 +358,7 @@ tidar_status step_attn_impl(const tidar_step_desc* d, const tidar_kv_cache* c, c
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = pth == 2   ? tidar::launch_attn_tc05(a, s)
-                  : pth == 3 ? tidar::launch_attn_dec(a, s)
+                  : pth == 3 ? (kv4 ? tidar::launch_attn_kv4_dec(a, s) : tidar::launch_attn_dec(a, s))
                   : pth == 4 ? tidar::launch_attn_pair(a, s)
                              : tidar::launch_attn_simt(a, s);
   if (e == cudaErrorNotSupported) return TIDAR_ERR_UNSUPPORTED;

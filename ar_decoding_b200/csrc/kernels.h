@@ -40,7 +40,10 @@ struct AttnArgs {
 // part_o / part_lse and launch_finalize merges and appends.
 cudaError_t launch_attn_dec(const AttnArgs& a, cudaStream_t s);
 int dec_resident_clusters(int ns, int M);   // M = packed query rows per KV head
-// CUDA-core kernel (fp32 or bf16, D 64 or 128).
+// The same for the 4-bit cache (bf16, D 128, any page size).
+cudaError_t launch_attn_kv4_dec(const AttnArgs& a, cudaStream_t s);
+int kv4_dec_resident_clusters(int ns, int M);
+// CUDA-core kernel (fp32 or bf16, D 64 or 128; either cache).
 cudaError_t launch_attn_simt(const AttnArgs& a, cudaStream_t s);
 // tcgen05/TMEM kernel (bf16, D 128, page 64).  Returns cudaErrorNotSupported if
 // the tensor maps cannot be built.
