@@ -24,14 +24,14 @@
 // (r % 8) / 2 + 4 (r % 2) + 8 (r / 8): the four keys whose values a lane loads
 // are then t, t+4, t+8, t+12 and the loads of a warp cover 256 contiguous bytes.
 //
-// Grid (split, b * Hkv).  Warp 0 produces: one bulk copy per page and operand
-// (two where a page is not 64 rows) into a ring of 64-key stages, no tensor
-// maps.  Compute warps take half a stage (32 keys) each in turn.  The running
-// maximum is only raised when a score passes it by 2^8, and only then do the
-// lanes exchange maxima.  Warps merge in shared memory; the splits of a prefix
-// merge on chip (cluster) or through workspace partials and the finalize
-// launch.  Every mbarrier wait is bounded (~1 s): on expiry the CTA records
-// TIDAR_DEVERR_TIMEOUT, the producer drains what it issued and the CTA exits.
+// Grid (split, b * Hkv).  Every warp runs its own pipeline: units of 32 keys in
+// turn, three slots of shared memory filled by 16-byte asynchronous copies, no
+// barrier between warps until the end.  (A producer warp with bulk or tiled
+// copies of whole pages could not issue fast enough: 9 KB stages at 2.7 and 3.3
+// TB/s with nothing but the copies running.)  The running maximum is only
+// raised when a score passes it by 2^8, and only then do the lanes exchange
+// maxima.  Warps merge in shared memory; the splits of a prefix merge on chip
+// (cluster) or through workspace partials and the finalize launch.
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
@@ -44,30 +44,27 @@ namespace {
 
 using tc05::kStageStride;
 
-// NT 8-row query tiles (1: M <= 8, 2: M <= 16) and the compute warps that their
+// NT 8-row query tiles (1: M <= 8, 2: M <= 16) and the warps that their
 // registers leave room for.
 template <int NT> struct Kv4Shape {
-  static constexpr int kWarps = NT == 1 ? 15 : 11;
-  static constexpr int kThreads = 32 * (1 + kWarps);
+  static constexpr int kWarps = NT == 1 ? 16 : 12;
+  static constexpr int kThreads = 32 * kWarps;
 };
-constexpr int kStages = 20;
-constexpr uint32_t kCodes = 64 * 64;                    // 64 keys of 128 dims
-constexpr uint32_t kScales = 64 * 8;
-constexpr uint32_t kOperand = kCodes + kScales;         // one page of 64 keys, as it lies in memory
-constexpr uint32_t kStage = 2 * kOperand;               // K then V
-constexpr uint32_t kOffBar = kStages * kStage;          // full[s], empty[s]
-constexpr uint32_t kOffMisc = kOffBar + 2 * kStages * 8;   // abort flag, then the stages' block masks
-constexpr uint32_t kSmem = kOffMisc + 4 * (1 + kStages);
-static_assert(kSmem <= 232448, "shared memory budget");
+constexpr int kSlots = 3;                               // units of 32 keys per warp: one in use, two in flight
+constexpr uint32_t kCodes = 32 * 64;                    // 32 keys of 128 dims
+constexpr uint32_t kScales = 32 * 8;
+constexpr uint32_t kUnit = 2 * (kCodes + kScales);      // K codes, V codes, K scales, V scales
+template <int NT> constexpr uint32_t ring_bytes() { return Kv4Shape<NT>::kWarps * kSlots * kUnit; }
+static_assert(ring_bytes<1>() <= 232448, "shared memory budget");
 // the merge reuses the ring: the staged rows (16-byte aligned, a whole number
 // of float4), then the warps' rows, their maxima and sums
 constexpr int kXo = 132;
 constexpr int kStaged = 16 * (kStageStride + 2);        // floats
 static_assert(kStaged % 4 == 0 && kXo % 4 == 0, "rows of float4");
 template <int NT> constexpr uint32_t merge_bytes() {
-  return 4u * (kStaged + Kv4Shape<NT>::kWarps * 8 * NT * (kXo + 2) + Kv4Shape<NT>::kWarps);
+  return 4u * (kStaged + Kv4Shape<NT>::kWarps * 8 * NT * (kXo + 2));
 }
-static_assert(merge_bytes<1>() <= kOffBar && merge_bytes<2>() <= kOffBar, "merge area fits the ring");
+static_assert(merge_bytes<1>() <= ring_bytes<1>() && merge_bytes<2>() <= ring_bytes<2>(), "merge area fits the ring");
 
 struct Kv4DecParams {
   AttnArgs a;
@@ -97,40 +94,22 @@ __device__ __forceinline__ uint32_t sub136_mul(uint32_t x, uint32_t s) {
   const __nv_bfloat162 v = __hmul2(c, *reinterpret_cast<const __nv_bfloat162*>(&s));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
 // Physical key of row r (0..15) of a 16-key MMA block.
 __device__ __forceinline__ int key_of_row(int r) { return ((r & 7) >> 1) + 4 * (r & 1) + (r & 8); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 
 template <int NT>
 __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel(const Kv4DecParams prm) {
   constexpr int kWarps = Kv4Shape<NT>::kWarps;
-  constexpr int kThreads = Kv4Shape<NT>::kThreads;
   constexpr int kRows = 8 * NT;
   constexpr unsigned kAll = 0xffffffffu;
   extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t sb = smem_u32(smem);
   const AttnArgs& a = prm.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x, g_head = blockIdx.y % a.Hkv;
-  auto full = [&](int s) -> uint32_t { return sb + kOffBar + 8u * s; };
-  auto empty = [&](int s) -> uint32_t { return sb + kOffBar + 8u * (kStages + s); };
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc);
-  volatile int* stage_mask = abort_flag + 1;             // bit q: keys 16q .. 16q+15 are on a mapped page
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full(s), 1u);
-      mbar_init(empty(s), 2u);
-    }
-    *abort_flag = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  }
-  __syncthreads();
   pdl_wait();
   pdl_trigger();
   const int b = longest_first(a.seq_lens, a.B, (int)blockIdx.y / a.Hkv);
@@ -142,85 +121,76 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
   }
   const int k0 = split * a.keys_per_split;               // a multiple of 64
   const int kend = min(P, k0 + a.keys_per_split);
-  const int nst = kend > k0 ? (kend - k0 + 63) / 64 : 0;  // stages of 64 keys
+  const int units = kend > k0 ? (kend - k0 + 31) / 32 : 0;
   const bool step = split == a.nsplit - 1 && a.step_keys;
   const int32_t* table = a.page_table + (size_t)b * a.max_pages;
-  const int ps = a.page_size;
+  const int ps = a.page_size, lps = 31 - __clz(ps);
 
   // rows of this CTA's result: normalised O, lse and validity (after the loop)
   float* ost = reinterpret_cast<float*>(smem);
   float* lst = ost + 16 * kStageStride;
   int* wst = reinterpret_cast<int*>(lst + 16);
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- producer
-    const int piece = ps < 64 ? ps : 64;                  // keys of a stage on one page
-    const int npc = 64 / piece;
-    const size_t page_bytes = kv4_page_bytes(ps, 128);
-    // table entries of this split, 32 at a time, one per lane, the next window loading
-    const int e_first = k0 / ps;
-    auto load_win = [&](int base) -> int { return e_first + base + lane < a.max_pages ? table[e_first + base + lane] : -1; };
-    int wb = 0, cur = load_win(0), nxt = load_win(32);
-    bool bad = false;
-    int issued = 0;
-    for (int i = 0; i < nst; ++i) {
-      const int s = i % kStages;
-      if (i >= kStages) {
-        bool ok = true;
-        if (lane == 0) ok = wait_bar(empty(s), (uint32_t)((i / kStages - 1) & 1), abort_flag, a.err);
-        if (!__shfl_sync(kAll, ok ? 1 : 0, 0)) break;
+  // ---- this warp's copies: units warp, warp + kWarps, .. of 32 keys, on one
+  // page (or two of 16 rows).  Every lane copies 16-byte pieces: four of K's
+  // codes, four of V's, one of a scale row.  The page ids of the next unit are
+  // loaded while this one's copies are issued.
+  const size_t page_bytes = kv4_page_bytes(ps, 128);
+  const uint8_t* kbase = static_cast<const uint8_t*>(a.k_pages) + (size_t)g_head * page_bytes;
+  const uint8_t* vbase = static_cast<const uint8_t*>(a.v_pages) + (size_t)g_head * page_bytes;
+  const size_t page_stride = (size_t)a.Hkv * page_bytes;
+  const uint32_t slot0 = smem_u32(smem) + (uint32_t)warp * (kSlots * kUnit);
+  bool bad = false;
+  // pages of the two 16-key blocks of unit u (-1: no key, or no valid page)
+  auto load_pages = [&](int u, int (&pg)[2]) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int key = k0 + 32 * u + 16 * q;
+      pg[q] = -1;
+      if (u < units && key < kend) {
+        pg[q] = table[key >> lps];
+        if (pg[q] < 0 || pg[q] >= a.num_pages) pg[q] = -1, bad = true;
       }
-      const uint32_t dst = sb + (uint32_t)s * kStage;
-      int mask = 0, npages = 0, mine = -1;                // mine: the page of this lane's piece
-      for (int p = 0; p < npc; ++p) {
-        const int key = k0 + 64 * i + p * piece;
-        if (key >= kend) break;
-        const int e = key / ps - e_first;
-        while (e >= wb + 32) { wb += 32; cur = nxt; nxt = load_win(wb + 32); }
-        const int page = __shfl_sync(kAll, cur, e - wb);
-        const bool ok = page >= 0 && page < a.num_pages;
-        if (ok) {
-          mask |= ((1 << (piece / 16)) - 1) << (p * piece / 16);
-          ++npages;
-        } else {
-          bad = true;
-        }
-        if (lane / 4 == p) mine = ok ? page : -1;
-      }
-      if (lane == 0) {
-        stage_mask[s] = mask;                             // published by the arrival on `full`
-        if (npages) mbar_expect_tx(full(s), (uint32_t)(npages * piece) * 144u);
-        else mbar_arrive(full(s));
-      }
-      __syncwarp();
-      // lane 4p + 2v + c: piece p of K (v = 0) or V, its codes (c = 0) or scales;
-      // a page of 64 rows lies as a stage's operand does and comes in one copy
-      if (mine >= 0) {
-        const int p = lane >> 2, v = (lane >> 1) & 1, c = lane & 1;
-        const uint8_t* base = static_cast<const uint8_t*>(v ? a.v_pages : a.k_pages) +
-                              ((size_t)mine * a.Hkv + g_head) * page_bytes;
-        const int row = (k0 + 64 * i + p * piece) % ps;
-        if (ps == 64) {
-          if (c == 0) bulk_load(dst + v * kOperand, base, kOperand, full(s));
-        } else if (c == 0) {
-          bulk_load(dst + v * kOperand + p * piece * 64, base + (size_t)row * 64, piece * 64u, full(s));
-        } else {
-          bulk_load(dst + v * kOperand + kCodes + p * piece * 8, base + (size_t)ps * 64 + (size_t)row * 8, piece * 8u,
-                    full(s));
-        }
-      }
-      issued = i + 1;
     }
-    if (lane == 0) {
-      if (bad) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
-      if (*abort_flag)       // drain: no copy may still write shared memory when the CTA moves on
-        for (int i = max(0, issued - kStages); i < issued; ++i)
-          wait_quiet(full(i % kStages), (uint32_t)((i / kStages) & 1));
+  };
+  // queues unit u's copies into a slot and returns which 16-key blocks it holds
+  auto issue = [&](int u, int sl, const int (&pg)[2]) -> int {
+    const uint32_t dst = slot0 + (uint32_t)sl * kUnit + 16u * lane;
+    const int r0 = (k0 + 32 * u) & (ps - 1), r1 = (k0 + 32 * u + 16) & (ps - 1);
+    const size_t o0 = pg[0] * (long long)page_stride, o1 = pg[1] * (long long)page_stride;
+    if (pg[0] >= 0) {
+      const size_t c = o0 + (size_t)r0 * 64 + 16 * lane;
+      cp_async16(dst, kbase + c);
+      cp_async16(dst + 512, kbase + c + 512);
+      cp_async16(dst + kCodes, vbase + c);
+      cp_async16(dst + kCodes + 512, vbase + c + 512);
     }
-    __syncwarp();
-  } else {
-    // ---------------------------------------------------------------- compute
-    const int wid = warp - 1, gq = lane >> 2, cq = lane & 3;
+    if (pg[1] >= 0) {
+      const size_t c = o1 + (size_t)r1 * 64 + 16 * lane;
+      cp_async16(dst + 1024, kbase + c);
+      cp_async16(dst + 1536, kbase + c + 512);
+      cp_async16(dst + kCodes + 1024, vbase + c);
+      cp_async16(dst + kCodes + 1536, vbase + c + 512);
+    }
+    // scales: lanes 0..15 K, 16..31 V; 8 lanes a block of 16 keys
+    const bool second = lane & 8;
+    if ((second ? pg[1] : pg[0]) >= 0)
+      cp_async16(dst + 2 * kCodes, (lane < 16 ? kbase : vbase) + (second ? o1 : o0) + (size_t)ps * 64 +
+                                       (size_t)(second ? r1 : r0) * 8 + 16 * (lane & 7));
+    return (pg[0] >= 0 ? 1 : 0) | (pg[1] >= 0 ? 2 : 0);
+  };
+  int pg[2];
+  int blocks = 0;                        // two bits per slot in flight, the oldest lowest
+#pragma unroll
+  for (int i = 0; i < kSlots - 1; ++i) {
+    load_pages(warp + i * kWarps, pg);
+    blocks |= issue(warp + i * kWarps, i, pg) << (2 * i);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  load_pages(warp + (kSlots - 1) * kWarps, pg);
+
+  {
+    const int wid = warp, gq = lane >> 2, cq = lane & 3;
     const float sl2 = prm.scale_log2;
     // Q^T as the B operand: qb[G][nt] = dims 32G + 8cq .. + 7 of row 8nt + gq,
     // two MMA steps of two registers each; qc = -136 times the groups' sums of
@@ -309,7 +279,7 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
       }
     };
 
-    if (step && wid == kWarps - 1) {
+    if (step && wid == kWarps - 1) {      // the warp with the fewest units
       // ---- the step keys (R <= 16 rows of k_blk / v_blk), fragments straight
       // from global memory; MMA row r is key_of_row(r)
       float sc[1][NT][4];
@@ -368,19 +338,26 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
       }
     }
 
-    // ---- the prefix: half a stage (32 keys) at a time
-    bool ok = true;
+    // ---- the prefix: a unit (32 keys) at a time
     const int krow = key_of_row(gq);
-    for (int u = wid; u < 2 * nst; u += kWarps) {
-      const int i = u >> 1, half = u & 1, s = i % kStages;
-      ok = warp_wait_bar(full(s), (uint32_t)((i / kStages) & 1), abort_flag, a.err);
-      if (!ok) break;
-      const uint8_t* kc = smem + (size_t)s * kStage + half * 32 * 64;
-      const uint8_t* ks = smem + (size_t)s * kStage + kCodes + half * 32 * 8;
-      const uint8_t* vc = kc + kOperand;
-      const uint8_t* vs = ks + kOperand;
-      const int nleft = kend - k0 - 64 * i - 32 * half;   // valid keys of this half (may be <= 0)
-      const int mask = (stage_mask[s] >> (2 * half)) & 3;
+    int sl = 0;
+    for (int u = wid; u < units; u += kWarps) {
+      // the slot freed last time takes the unit after the ones in flight
+      {
+        const int nu = u + (kSlots - 1) * kWarps, ns = sl == 0 ? kSlots - 1 : sl - 1;
+        blocks |= issue(nu, ns, pg) << (2 * (kSlots - 1));
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        load_pages(nu + kWarps, pg);
+      }
+      asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
+      __syncwarp();
+      const int mask = blocks & 3;
+      blocks >>= 2;
+      const uint8_t* kc = smem + (size_t)warp * (kSlots * kUnit) + (size_t)sl * kUnit;
+      const uint8_t* vc = kc + kCodes;
+      const uint8_t* ks = vc + kCodes;
+      const uint8_t* vs = ks + kScales;
+      const int nleft = kend - k0 - 32 * u;              // valid keys of this unit
       float sc[2][NT][4];
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
@@ -457,9 +434,10 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
                        pb[kb][nt][1]);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(s));
+      __syncwarp();                       // every lane has read the slot: it may be refilled
+      if (++sl == kSlots) sl = 0;
     }
+    if (bad) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
 
     // ---- merge the warps: (max, sum, O) per row through the idle ring
 #pragma unroll
@@ -470,11 +448,11 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
         l[nt][h] += __shfl_xor_sync(kAll, l[nt][h], 8);
         l[nt][h] += __shfl_xor_sync(kAll, l[nt][h], 16);
       }
-    asm volatile("bar.sync 1, %0;" ::"r"(32 * kWarps) : "memory");   // every warp is past its last stage
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();                      // every warp is past its last unit
     float* xo = reinterpret_cast<float*>(smem) + kStaged;             // [warps][kRows][kXo]
     float* xm = xo + kWarps * kRows * kXo;                            // [warps][kRows]
     float* xl = xm + kWarps * kRows;
-    int* xk = reinterpret_cast<int*>(xl + kWarps * kRows);            // [warps]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -493,11 +471,7 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
           }
         }
       }
-    if (lane == 0) xk[wid] = ok ? 1 : 0;
-    asm volatile("bar.sync 1, %0;" ::"r"(32 * kWarps) : "memory");
-    bool all_ok = true;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) all_ok = all_ok && xk[w];
+    __syncthreads();
     for (int r = wid; r < prm.M; r += kWarps) {
       float top = -INFINITY;
 #pragma unroll
@@ -521,8 +495,8 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
       const float inv = any ? 1.f / lt : 0.f;
       *reinterpret_cast<float4*>(ost + r * kStageStride + 4 * lane) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
       if (lane == 0) {
-        lst[r] = any && all_ok ? (top + log2f(lt)) * 0.69314718055994531f : -INFINITY;
-        wst[r] = all_ok ? 1 : 0;
+        lst[r] = any ? (top + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+        wst[r] = 1;
       }
     }
   }
@@ -551,7 +525,7 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
 
   if (split == 0 && len_ok && (a.nsplit == 1 || a.cluster_merge) && a.append) {
     // draft rows D_1..D_n of this head, quantised: a quad per (row, K or V)
-    for (int u0 = warp * 8; u0 < 2 * a.n; u0 += 8 * (kThreads / 32)) {
+    for (int u0 = warp * 8; u0 < 2 * a.n; u0 += 8 * kWarps) {
       const int u = u0 + (lane >> 2), r = u >> 1, y = lane & 3;
       const bool in = u < 2 * a.n, is_key = !(u & 1);
       const int pos = P + (in ? r : 0);
@@ -578,7 +552,7 @@ cudaError_t smem_attr() {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorNotSupported;
   if (!set[dev]) {
-    e = cudaFuncSetAttribute(attn_kv4_dec_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(attn_kv4_dec_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes<NT>());
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
@@ -599,7 +573,7 @@ int resident_clusters_t(int ns) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ns, 1, 1);
     cfg.blockDim = dim3(Kv4Shape<NT>::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = ring_bytes<NT>();
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = ns;
@@ -634,8 +608,8 @@ cudaError_t launch_attn_kv4_dec(const AttnArgs& a, cudaStream_t s) {
   cudaError_t e = M <= 8 ? smem_attr<1>() : smem_attr<2>();
   if (e != cudaSuccess) return e;
   if (M <= 8)
-    return launch_clustered(attn_kv4_dec_kernel<1>, grid, cluster, Kv4Shape<1>::kThreads, kSmem, s, prm);
-  return launch_clustered(attn_kv4_dec_kernel<2>, grid, cluster, Kv4Shape<2>::kThreads, kSmem, s, prm);
+    return launch_clustered(attn_kv4_dec_kernel<1>, grid, cluster, Kv4Shape<1>::kThreads, ring_bytes<1>(), s, prm);
+  return launch_clustered(attn_kv4_dec_kernel<2>, grid, cluster, Kv4Shape<2>::kThreads, ring_bytes<2>(), s, prm);
 }
 
 }  // namespace tidar
