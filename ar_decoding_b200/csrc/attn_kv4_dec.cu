@@ -85,9 +85,14 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-// Pair i of a word of codes as the bf16 numbers 136 + c.
+// Pair i of a word of codes as the bf16 numbers 136 + c: one shift and one
+// three-input logic instruction, (x & 0x000f000f) ^ 0x43084308 (left to the
+// compiler, the two constants cost two instructions; the integer pipe, at half
+// the issue rate, is what bounds this kernel).
 __device__ __forceinline__ uint32_t offset_codes(uint32_t w, int i) {
-  return ((w >> (4 * i)) & 0x000f000fu) ^ 0x43084308u;
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(0x43084308u));
+  return r;
 }
 __device__ __forceinline__ uint32_t sub136_mul(uint32_t x, uint32_t s) {
   const __nv_bfloat162 c = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), __float2bfloat162_rn(136.f));
