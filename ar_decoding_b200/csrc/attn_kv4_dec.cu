@@ -80,6 +80,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// D = A * B + C with both rows of C equal to (c0, c1).
+__device__ __forceinline__ void mma16816_c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                           uint32_t b1, float c0, float c1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %10, %11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -138,50 +147,59 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
 
   // ---- this warp's copies: units warp, warp + kWarps, .. of 32 keys, on one
   // page (or two of 16 rows).  Every lane copies 16-byte pieces: four of K's
-  // codes, four of V's, one of a scale row.  The page ids of the next unit are
-  // loaded while this one's copies are issued.
+  // codes, four of V's, one of a scale row (lanes 0..15 K, 16..31 V).  The page
+  // id of the next unit is loaded while this one's copies are issued.
   const size_t page_bytes = kv4_page_bytes(ps, 128);
-  const uint8_t* kbase = static_cast<const uint8_t*>(a.k_pages) + (size_t)g_head * page_bytes;
-  const uint8_t* vbase = static_cast<const uint8_t*>(a.v_pages) + (size_t)g_head * page_bytes;
   const size_t page_stride = (size_t)a.Hkv * page_bytes;
-  const uint32_t slot0 = smem_u32(smem) + (uint32_t)warp * (kSlots * kUnit);
+  const uint8_t* kcodes = static_cast<const uint8_t*>(a.k_pages) + (size_t)g_head * page_bytes + 16 * lane;
+  const uint8_t* vcodes = static_cast<const uint8_t*>(a.v_pages) + (size_t)g_head * page_bytes + 16 * lane;
+  const uint8_t* scales = static_cast<const uint8_t*>(lane < 16 ? a.k_pages : a.v_pages) + (size_t)g_head * page_bytes +
+                          (size_t)ps * 64 + 16 * (ps == 16 ? lane & 7 : lane & 15);
+  const uint32_t slot0 = smem_u32(smem) + (uint32_t)warp * (kSlots * kUnit) + 16u * lane;
+  const int half = ps == 16 ? (lane >> 3) & 1 : 0;        // 16-row pages: the block whose scales this lane copies
   bool bad = false;
-  // pages of the two 16-key blocks of unit u (-1: no key, or no valid page)
-  auto load_pages = [&](int u, int (&pg)[2]) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int key = k0 + 32 * u + 16 * q;
-      pg[q] = -1;
-      if (u < units && key < kend) {
-        pg[q] = table[key >> lps];
-        if (pg[q] < 0 || pg[q] >= a.num_pages) pg[q] = -1, bad = true;
-      }
+  // page of block q of unit u (-1: no key, or no valid page)
+  auto load_page = [&](int u, int q) -> int {
+    const int key = k0 + 32 * u + 16 * q;
+    int pg = -1;
+    if (key < kend) {
+      pg = table[key >> lps];
+      if (pg < 0 || pg >= a.num_pages) pg = -1, bad = true;
     }
+    return pg;
+  };
+  auto load_pages = [&](int u, int (&pg)[2]) {
+    pg[0] = load_page(u, 0);
+    pg[1] = ps == 16 ? load_page(u, 1) : pg[0];
   };
   // queues unit u's copies into a slot and returns which 16-key blocks it holds
   auto issue = [&](int u, int sl, const int (&pg)[2]) -> int {
-    const uint32_t dst = slot0 + (uint32_t)sl * kUnit + 16u * lane;
-    const int r0 = (k0 + 32 * u) & (ps - 1), r1 = (k0 + 32 * u + 16) & (ps - 1);
-    const size_t o0 = pg[0] * (long long)page_stride, o1 = pg[1] * (long long)page_stride;
-    if (pg[0] >= 0) {
-      const size_t c = o0 + (size_t)r0 * 64 + 16 * lane;
-      cp_async16(dst, kbase + c);
-      cp_async16(dst + 512, kbase + c + 512);
-      cp_async16(dst + kCodes, vbase + c);
-      cp_async16(dst + kCodes + 512, vbase + c + 512);
+    const uint32_t dst = slot0 + (uint32_t)sl * kUnit;
+    const uint32_t row = (uint32_t)(k0 + 32 * u) & (uint32_t)(ps - 1);
+    if (ps != 16) {
+      if (pg[0] < 0) return 0;
+      const size_t at = (size_t)pg[0] * page_stride;
+      const uint8_t* kc = kcodes + at + row * 64;
+      const uint8_t* vc = vcodes + at + row * 64;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        cp_async16(dst + 512 * j, kc + 512 * j);
+        cp_async16(dst + kCodes + 512 * j, vc + 512 * j);
+      }
+      cp_async16(dst + 2 * kCodes, scales + at + row * 8);
+      return 3;
     }
-    if (pg[1] >= 0) {
-      const size_t c = o1 + (size_t)r1 * 64 + 16 * lane;
-      cp_async16(dst + 1024, kbase + c);
-      cp_async16(dst + 1536, kbase + c + 512);
-      cp_async16(dst + kCodes + 1024, vbase + c);
-      cp_async16(dst + kCodes + 1536, vbase + c + 512);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (pg[q] < 0) continue;
+      const size_t at = (size_t)pg[q] * page_stride;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        cp_async16(dst + 1024 * q + 512 * j, kcodes + at + 512 * j);
+        cp_async16(dst + kCodes + 1024 * q + 512 * j, vcodes + at + 512 * j);
+      }
+      if (half == q) cp_async16(dst + 2 * kCodes, scales + at);
     }
-    // scales: lanes 0..15 K, 16..31 V; 8 lanes a block of 16 keys
-    const bool second = lane & 8;
-    if ((second ? pg[1] : pg[0]) >= 0)
-      cp_async16(dst + 2 * kCodes, (lane < 16 ? kbase : vbase) + (second ? o1 : o0) + (size_t)ps * 64 +
-                                       (size_t)(second ? r1 : r0) * 8 + 16 * (lane & 7));
     return (pg[0] >= 0 ? 1 : 0) | (pg[1] >= 0 ? 2 : 0);
   };
   int pg[2];
@@ -229,9 +247,14 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
     for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
-    float m[NT][2], l[NT][2];
+    // running maximum (log2 domain), its negative as the exponent's offset (0
+    // while there is none), and the raw score past which it is raised
+    float m[NT][2], l[NT][2], negm[NT][2], lim[NT][2];
+    const float inv_sl2 = 1.f / sl2;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) m[nt][h] = lim[nt][h] = -INFINITY, l[nt][h] = negm[nt][h] = 0.f;
 
     // Online softmax of KB blocks of 16 keys: sc holds raw scores (-inf where
     // masked) on entry; pb the P^T operands on return.
@@ -245,7 +268,7 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
           float mx = -INFINITY;
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb) mx = fmaxf(mx, fmaxf(sc[kb][nt][h], sc[kb][nt][h + 2]));
-          up = up || mx * sl2 > m[nt][h] + 8.f;
+          up = up || mx > lim[nt][h];
         }
       if (__any_sync(kAll, up)) {
 #pragma unroll
@@ -261,6 +284,8 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
             const float nm = fmaxf(m[nt][h], mx * sl2);
             const float f = m[nt][h] == -INFINITY ? 0.f : ex2(m[nt][h] - nm);
             m[nt][h] = nm;
+            negm[nt][h] = nm == -INFINITY ? 0.f : -nm;
+            lim[nt][h] = (nm + 8.f) * inv_sl2;
             l[nt][h] *= f;
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
@@ -271,7 +296,7 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float n0 = m[nt][0] == -INFINITY ? 0.f : -m[nt][0], n1 = m[nt][1] == -INFINITY ? 0.f : -m[nt][1];
+        const float n0 = negm[nt][0], n1 = negm[nt][1];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
           const float p0 = ex2(fmaf(sc[kb][nt][0], sl2, n0)), p1 = ex2(fmaf(sc[kb][nt][1], sl2, n1));
@@ -382,8 +407,8 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
           for (int e = 0; e < 4; ++e) ra[e] = offset_codes(wa[G], e), rd[e] = offset_codes(wd[G], e);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float acc[4] = {qc[G][nt][0], qc[G][nt][1], qc[G][nt][0], qc[G][nt][1]};
-            mma16816(acc, ra[0], rd[0], ra[1], rd[1], qb[G][nt][0], qb[G][nt][1]);
+            float acc[4];
+            mma16816_c(acc, ra[0], rd[0], ra[1], rd[1], qb[G][nt][0], qb[G][nt][1], qc[G][nt][0], qc[G][nt][1]);
             mma16816(acc, ra[2], rd[2], ra[3], rd[3], qb[G][nt][2], qb[G][nt][3]);
             if (G == 0) {
               sc[kb][nt][0] = acc[0] * fa[0]; sc[kb][nt][1] = acc[1] * fa[0];
@@ -397,6 +422,10 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
       }
       const bool whole = mask == 3 && nleft >= 32;
       if (!whole) {
+        // a masked key's value scales may be anything, and 0 times a NaN is not 0
+        if (lane >= nleft || !((mask >> (lane >> 4)) & 1))
+          *reinterpret_cast<uint2*>(smem + (vs - smem) + lane * 8) = make_uint2(0, 0);
+        __syncwarp();
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -417,8 +446,6 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
         for (int e = 0; e < 4; ++e) {
           c[e] = *reinterpret_cast<const uint2*>(vc + (16 * kb + cq + 4 * e) * 64 + gq * 8);
           t[e] = *reinterpret_cast<const uint2*>(vs + (16 * kb + cq + 4 * e) * 8);
-          // a masked key's scale bytes may be anything: p = 0 times a NaN is not 0
-          if (!whole && (16 * kb + cq + 4 * e >= nleft || !((mask >> kb) & 1))) t[e] = make_uint2(0, 0);
         }
 #pragma unroll
         for (int G = 0; G < 4; ++G) {
