@@ -96,7 +96,7 @@ tidar_status check_cache(const tidar_step_desc* d, const tidar_kv_cache* c) {
 constexpr bool kTc05Built = true;
 
 bool tc05_supported(const tidar_step_desc* d, bool kv4 = false) {
-  if (kv4) return false;
+  if (kv4) return kTc05Built && d->dtype == TIDAR_BF16 && d->head_dim == 128 && d->num_q_heads / d->num_kv_heads <= 128;
   return kTc05Built && d->dtype == TIDAR_BF16 && d->head_dim == 128 && d->page_size == 64;
 }
 
@@ -224,7 +224,7 @@ Plan make_plan(const tidar_step_desc* d, int path, bool kv4 = false) {
     const double cost_p = (double)((ctas + target - 1) / target) * per + (p.nsplit > 1 ? kFinalizeBlocks : 0.0);
     if (cost_p < best) { best = cost_p; best_n = n; best_cluster = false; }
     if (p.nsplit > 1 && p.nsplit <= 16 && !g_force_partials) {
-      const int resident = path == 2 ? tidar::tc05_resident_clusters(p.nsplit)
+      const int resident = path == 2 ? tidar::tc05_resident_clusters(p.nsplit, kv4)
                                      : path == 4 ? tidar::pair_resident_clusters(p.nsplit)
                            : kv4       ? tidar::kv4_dec_resident_clusters(p.nsplit, M)
                                        : tidar::dec_resident_clusters(p.nsplit, M);

@@ -25,7 +25,7 @@
 // are then t, t+4, t+8, t+12 and the loads of a warp cover 256 contiguous bytes.
 //
 // Grid (split, b * Hkv).  Every warp runs its own pipeline: units of 32 keys in
-// turn, three slots of shared memory filled by 16-byte asynchronous copies, no
+// turn, two slots of shared memory filled by 16-byte asynchronous copies, no
 // barrier between warps until the end.  (A producer warp with bulk or tiled
 // copies of whole pages could not issue fast enough: 9 KB stages at 2.7 and 3.3
 // TB/s with nothing but the copies running.)  The running maximum is only
@@ -47,15 +47,14 @@ using tc05::kStageStride;
 // NT 8-row query tiles (1: M <= 8, 2: M <= 16) and the warps that their
 // registers leave room for.
 template <int NT> struct Kv4Shape {
-  static constexpr int kWarps = NT == 1 ? 16 : 12;
+  static constexpr int kWarps = NT == 1 ? 16 : 8;
   static constexpr int kThreads = 32 * kWarps;
 };
-constexpr int kSlots = 3;                               // units of 32 keys per warp: one in use, two in flight
+constexpr int kSlots = 2;                               // units of 32 keys per warp: one in use, one in flight
 constexpr uint32_t kCodes = 32 * 64;                    // 32 keys of 128 dims
 constexpr uint32_t kScales = 32 * 8;
 constexpr uint32_t kUnit = 2 * (kCodes + kScales);      // K codes, V codes, K scales, V scales
 template <int NT> constexpr uint32_t ring_bytes() { return Kv4Shape<NT>::kWarps * kSlots * kUnit; }
-static_assert(ring_bytes<1>() <= 232448, "shared memory budget");
 // the merge reuses the ring: the staged rows (16-byte aligned, a whole number
 // of float4), then the warps' rows, their maxima and sums
 constexpr int kXo = 132;
@@ -64,7 +63,10 @@ static_assert(kStaged % 4 == 0 && kXo % 4 == 0, "rows of float4");
 template <int NT> constexpr uint32_t merge_bytes() {
   return 4u * (kStaged + Kv4Shape<NT>::kWarps * 8 * NT * (kXo + 2));
 }
-static_assert(merge_bytes<1>() <= ring_bytes<1>() && merge_bytes<2>() <= ring_bytes<2>(), "merge area fits the ring");
+template <int NT> constexpr uint32_t smem_bytes() {
+  return merge_bytes<NT>() > ring_bytes<NT>() ? merge_bytes<NT>() : ring_bytes<NT>();
+}
+static_assert(smem_bytes<1>() <= 232448 && smem_bytes<2>() <= 232448, "shared memory budget");
 
 struct Kv4DecParams {
   AttnArgs a;
@@ -584,7 +586,7 @@ cudaError_t smem_attr() {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorNotSupported;
   if (!set[dev]) {
-    e = cudaFuncSetAttribute(attn_kv4_dec_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes<NT>());
+    e = cudaFuncSetAttribute(attn_kv4_dec_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NT>());
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
@@ -605,7 +607,7 @@ int resident_clusters_t(int ns) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ns, 1, 1);
     cfg.blockDim = dim3(Kv4Shape<NT>::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = ring_bytes<NT>();
+    cfg.dynamicSmemBytes = smem_bytes<NT>();
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = ns;
@@ -640,8 +642,8 @@ cudaError_t launch_attn_kv4_dec(const AttnArgs& a, cudaStream_t s) {
   cudaError_t e = M <= 8 ? smem_attr<1>() : smem_attr<2>();
   if (e != cudaSuccess) return e;
   if (M <= 8)
-    return launch_clustered(attn_kv4_dec_kernel<1>, grid, cluster, Kv4Shape<1>::kThreads, ring_bytes<1>(), s, prm);
-  return launch_clustered(attn_kv4_dec_kernel<2>, grid, cluster, Kv4Shape<2>::kThreads, ring_bytes<2>(), s, prm);
+    return launch_clustered(attn_kv4_dec_kernel<1>, grid, cluster, Kv4Shape<1>::kThreads, smem_bytes<1>(), s, prm);
+  return launch_clustered(attn_kv4_dec_kernel<2>, grid, cluster, Kv4Shape<2>::kThreads, smem_bytes<2>(), s, prm);
 }
 
 }  // namespace tidar

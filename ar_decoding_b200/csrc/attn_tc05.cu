@@ -36,6 +36,14 @@
 // merge in this kernel (cluster_merge: each CTA stages its normalised rows in
 // shared memory and owners read their peers' rows over distributed shared
 // memory), or write fp32 partials to the workspace for a finalize launch.
+// KV4 (the 4-bit cache of kv4.cuh, any page size): 20 warps.  Warp 0 is the MMA
+// issuer, warps 1..3 take the producer's place for prefix blocks: they copy
+// codes and scales in groups of 8 keys (asynchronous copies, twelve groups
+// ahead each), turn them into the bf16 values they stand for (exact) and write
+// those into the K and V rings in the layout that TMA would have left, in the
+// order K0, K1, V0, K2, V1, ..; warps 4..19 are the softmax warps.  Step-key
+// windows still come by TMA.  A V ring of two stages makes room for the raw
+// groups.  With 20 warps every thread may hold 96 registers, as in the bf16 form.
 // Every mbarrier wait is bounded: on expiry the CTA records TIDAR_DEVERR_TIMEOUT,
 // stops issuing, drains what it issued (bounded), frees TMEM and exits.
 #include <cuda.h>
@@ -43,6 +51,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "kv4.cuh"
 #include "sm100.cuh"
 #include "tc05.cuh"
 
@@ -50,15 +59,9 @@ namespace tidar {
 
 namespace {
 
-constexpr int kThreads = 576;       // producer, MMA, 16 softmax warps
-constexpr int kStages = 3;       // K/V ring depth; also the number of S buffers
-
+constexpr int kStages = 3;       // K ring depth
 constexpr uint32_t kChunkBytes = 16384;                 // 128 rows x 128 B (64 bf16)
 constexpr uint32_t kTileBytes = 2 * kChunkBytes;        // 128 x 128 bf16
-constexpr uint32_t kOffQ = 0;
-constexpr uint32_t kOffK = kOffQ + kTileBytes;
-constexpr uint32_t kOffV = kOffK + kStages * kTileBytes;
-constexpr uint32_t kOffBar = kOffV + kStages * kTileBytes;
 // barrier indices
 constexpr int BAR_Q = 0;
 constexpr int BAR_KFULL = 1;     // + stage
@@ -70,12 +73,28 @@ constexpr int BAR_PVDONE = 16;   // + S buffer
 constexpr int BAR_FINAL = 19;
 constexpr int BAR_VEMPTY = 20;   // + stage: V stage free again (its PV MMA is done)
 constexpr int kNumBars = 23;
-constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;   // [0] TMEM base, [1] abort flag
-constexpr uint32_t kOffRed = kOffMisc + 16;              // softmax halves: maxima [2][2][128] f32
-constexpr uint32_t kOffOk = kOffRed + 2048;              // and warp status [2][2][4] i32
-constexpr uint32_t kSmemUsed = kOffOk + 64;
-constexpr uint32_t kSmemAlloc = kSmemUsed;               // the dynamic window is 1024-byte aligned
-static_assert(kSmemAlloc <= 232448, "shared memory budget");
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffK = kOffQ + kTileBytes;
+constexpr uint32_t kOffV = kOffK + kStages * kTileBytes;
+// KV4: dequantising warps, and each one's ring of raw groups of 8 keys
+constexpr int kDqWarps = 3;
+constexpr int kRawDepth = 12;
+constexpr uint32_t kRawGroup = 8 * 72;                  // codes, then scales
+// Warp roles and the shared-memory layout behind the rings.
+template <bool KV4> struct Tc {
+  static constexpr int kThreads = KV4 ? 640 : 576;
+  static constexpr int kMma = KV4 ? 0 : 1;              // MMA issuer and TMEM owner
+  static constexpr int kSoft0 = KV4 ? 1 + kDqWarps : 2; // first of the 16 softmax warps
+  static constexpr int kVStages = KV4 ? 2 : kStages;
+  static constexpr int kFull = KV4 ? kDqWarps : 1;      // arrivals that fill a stage
+  static constexpr uint32_t kOffRaw = kOffV + kVStages * kTileBytes;
+  static constexpr uint32_t kOffBar = kOffRaw + (KV4 ? kDqWarps * kRawDepth * kRawGroup : 0);
+  static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;   // [0] TMEM base, [1] abort flag
+  static constexpr uint32_t kOffRed = kOffMisc + 16;             // softmax halves: maxima [2][2][128] f32
+  static constexpr uint32_t kOffOk = kOffRed + 2048;             // and warp status [2][2][4] i32
+  static constexpr uint32_t kSmem = kOffOk + 64;                 // the dynamic window is 1024-byte aligned
+};
+static_assert(Tc<false>::kSmem <= 232448 && Tc<true>::kSmem <= 232448, "shared memory budget");
 
 constexpr uint32_t kTmemCols = 512;
 // Softmax set t (block parity) owns S_t (P_t is written over its first 64
@@ -124,13 +143,195 @@ __device__ __forceinline__ bool trace_cta() { return blockIdx.x == 0 && blockIdx
 using namespace tc05;
 static_assert((128 * kStageStride + 256) * 4 <= kStages * kTileBytes, "row staging fits the K ring");
 
+// ------------------------------------------------------------------ 4-bit cache
+// The dequantising warps (1 .. kDqWarps) of a KV4 CTA: Q, then the blocks of
+// the K and V rings.  A group is 8 neighbouring keys of one operand; lane
+// (kk, y), kk = (lane/8) + 4 (lane/4 % 2), y = lane % 4, copies and converts
+// chunk y of key kk: eight dims of each of the four groups of 32, 16 bytes of
+// bf16 each.  Eight lanes then hold keys k and k + 4, whose swizzled 16-byte
+// units fall into different halves of the 128-byte row: stores without bank
+// conflicts.  Twelve groups (6.9 KB) a warp in flight; converting a block of
+// 128 keys is 32 groups of about 85 instructions over the three warps.
+__device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensorMap& tm_q, const CUtensorMap& tm_ks,
+                                           const CUtensorMap& tm_vs, uint8_t* smem, uint32_t sb, const BlockPlan& bp,
+                                           const int32_t* table, int b, int g, int rho0, volatile int* abort_flag) {
+  using L = Tc<true>;
+  const AttnArgs& a = prm.a;
+  const int w = ((int)threadIdx.x >> 5) - 1, lane = (int)threadIdx.x & 31;
+  auto bar = [&](int i) -> uint32_t { return sb + L::kOffBar + 8u * i; };
+  if (w == 0 && lane == 0) {
+    mbar_expect_tx(bar(BAR_Q), 2u * 128u * (uint32_t)(prm.rho_per_tile * a.G));
+    tma_load_4d(sb + kOffQ, &tm_q, 0, g * a.G, rho0, b, bar(BAR_Q));
+    tma_load_4d(sb + kOffQ + kChunkBytes, &tm_q, 64, g * a.G, rho0, b, bar(BAR_Q));
+  }
+  const int ps = a.page_size, lps = 31 - __clz(ps);
+  const size_t page_bytes = kv4_page_bytes(ps, 128), page_stride = (size_t)a.Hkv * page_bytes;
+  const uint8_t* kbase = static_cast<const uint8_t*>(a.k_pages) + (size_t)g * page_bytes;
+  const uint8_t* vbase = static_cast<const uint8_t*>(a.v_pages) + (size_t)g * page_bytes;
+  const int kk = ((lane >> 3) & 3) + 4 * ((lane >> 2) & 1), y = lane & 3;
+  const uint32_t raw0 = L::kOffRaw + (uint32_t)w * (kRawDepth * kRawGroup);
+  // Phase p of the conversion: K(0); then for j = 1, 2, ..: K(j) at 2j - 1 and
+  // V(j - 1) at 2j, up to V(nb - 1).  Block of phase p, -1 for K past the last.
+  const int phases = 2 * bp.nb + 1;
+  auto block_of = [&](int p) -> int { return p == 0 ? 0 : (p & 1) ? ((p + 1) / 2 < bp.nb ? (p + 1) / 2 : -1) : p / 2 - 1; };
+  auto is_v = [&](int p) -> bool { return p > 0 && !(p & 1); };
+  auto has_groups = [&](int p) -> bool { const int i = block_of(p); return i >= 0 && i < bp.npb; };
+  // The copies run ahead along the same sequence of (phase, group): this warp's
+  // groups of phase p are (w + p) % 3, + 3, ..
+  bool bad = false;
+  uint32_t slot_ok = 0;
+  int ip = 0, ig = w, slot_i = 0, pg_next = -1;
+  auto settle = [&]() {           // moves the copy iterator to a phase that has groups
+    while (ip < phases && (!has_groups(ip) || ig >= 16)) {
+      ++ip;
+      ig = (w + ip) % 3;
+    }
+  };
+  auto load_page = [&]() -> int { // page of the copy iterator's group (-1: none)
+    if (ip >= phases) return -1;
+    const int key = bp.k0 + 128 * block_of(ip) + 8 * ig;
+    if (key >= bp.kend) return -1;
+    const int pg = table[key >> lps];
+    if (page_ok(pg, a.num_pages)) return pg;
+    bad = true;
+    return -1;
+  };
+  auto copy_one = [&]() {
+    if (ip < phases) {
+      const int key = bp.k0 + 128 * block_of(ip) + 8 * ig, pg = pg_next;
+      if (pg >= 0) {
+        const int row = key & (ps - 1);
+        const uint8_t* base = (is_v(ip) ? vbase : kbase) + (size_t)pg * page_stride;
+        const uint32_t dst = sb + raw0 + (uint32_t)slot_i * kRawGroup;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16u * lane), "l"(base + (size_t)row * 64 + kk * 64 + y * 16)
+                     : "memory");
+        if (lane < 4)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512u + 16u * lane),
+                       "l"(base + (size_t)ps * 64 + (size_t)row * 8 + 16 * lane)
+                       : "memory");
+      }
+      // one bit a slot: the group lies on a valid page
+      slot_ok = (slot_ok & ~(1u << slot_i)) | ((pg >= 0 ? 1u : 0u) << slot_i);
+      ig += 3;
+      settle();
+      pg_next = load_page();
+      if (++slot_i == kRawDepth) slot_i = 0;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  settle();
+  pg_next = load_page();
+  if (!prm.starve)
+    for (int i = 0; i < kRawDepth - 1; ++i) copy_one();
+
+  int slot = 0;
+  bool ok = !prm.starve;
+  for (int p = 0; ok && p < phases; ++p) {
+    const int i = block_of(p);
+    if (i < 0) continue;
+    const bool v = is_v(p);
+    const int ns = v ? L::kVStages : kStages, s = i % ns;
+    const uint32_t full = bar((v ? BAR_VFULL : BAR_KFULL) + s);
+    if (i >= ns) ok = warp_wait_bar(bar((v ? BAR_VEMPTY : BAR_KEMPTY) + s), (uint32_t)((i / ns - 1) & 1), abort_flag, a.err);
+    if (!ok) break;
+    const uint32_t tile = (v ? kOffV : kOffK) + (uint32_t)s * kTileBytes;
+    if (i >= bp.npb) {
+      if (lane == 0) {
+        if (w == 0) {
+          const CUtensorMap* map = v ? &tm_vs : &tm_ks;
+          const int win = bp.wins[i - bp.npb];
+          mbar_expect_tx(full, kTileBytes);
+          tma_load_4d(sb + tile, map, 0, g, win * 128, b, full);
+          tma_load_4d(sb + tile + kChunkBytes, map, 64, g, win * 128, b, full);
+        } else {
+          mbar_arrive(full);
+        }
+      }
+      __syncwarp();
+      continue;
+    }
+    for (int q = (w + p) % 3; q < 16; q += 3) {
+      copy_one();                                          // refills the slot that the last group left
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRawDepth - 1) : "memory");
+      __syncwarp();
+      const uint8_t* raw = smem + raw0 + (uint32_t)slot * kRawGroup;
+      const int key = 8 * q + kk;
+      uint4 c = *reinterpret_cast<const uint4*>(raw + 16 * lane);
+      uint2 sc = *reinterpret_cast<const uint2*>(raw + 512 + 8 * kk);
+      const bool live = ((slot_ok >> slot) & 1u) && bp.k0 + 128 * i + key < bp.kend;
+      if (!live) c = make_uint4(0, 0, 0, 0), sc = make_uint2(0, 0);
+      uint32_t words[4] = {c.x, c.y, c.z, c.w};
+      if (v) {
+        const uint32_t raw4[4] = {c.x, c.y, c.z, c.w};
+        kv4_value_to_key<4>(raw4, words);
+      }
+      const uint32_t sp[4] = {__byte_perm(sc.x, 0, 0x1010), __byte_perm(sc.x, 0, 0x3232), __byte_perm(sc.y, 0, 0x1010),
+                              __byte_perm(sc.y, 0, 0x3232)};
+      uint8_t* row = smem + tile + key * 128;
+#pragma unroll
+      for (int G = 0; G < 4; ++G) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 x = __hmul2(kv4_codes2(words[G], e), *reinterpret_cast<const __nv_bfloat162*>(&sp[G]));
+          o[e] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+        *reinterpret_cast<uint4*>(row + (G >> 1) * kChunkBytes + (((4 * (G & 1) + y) ^ (key & 7)) << 4)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      __syncwarp();                                        // every lane has read the slot's scales
+      if (++slot == kRawDepth) slot = 0;
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (bad) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
+  if (w == 0 && lane == 0 && *abort_flag) {
+    // drain: no copy may still write shared memory when the CTA moves on
+    wait_quiet(bar(BAR_Q), 0);
+    for (int i = max(0, bp.nb - kStages); i < bp.nb; ++i) {
+      if (i < bp.npb) continue;
+      wait_quiet(bar(BAR_KFULL + i % kStages), (uint32_t)((i / kStages) & 1));
+      wait_quiet(bar(BAR_VFULL + i % L::kVStages), (uint32_t)((i / L::kVStages) & 1));
+    }
+  }
+  __syncwarp();
+}
+
+// Draft rows D_1..D_n of KV head g, quantised, into cache rows P .. P+n-1: four
+// lanes per (row, K or V).
+__device__ __forceinline__ void append_kv4(const AttnArgs& a, const int32_t* table, int b, int g, int P) {
+  const int lane = (int)threadIdx.x & 31, y = lane & 3, ps = a.page_size;
+  for (int u0 = ((int)threadIdx.x >> 5) * 8; u0 < 2 * a.n; u0 += 8 * ((int)blockDim.x >> 5)) {
+    const int u = u0 + (lane >> 2), r = u < 2 * a.n ? u >> 1 : 0;
+    const bool in = u < 2 * a.n, is_key = !(u & 1);
+    const int pos = P + r, page = table[pos / ps];
+    const bool mapped = page_ok(page, a.num_pages);
+    if (in && !mapped && y == 0) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_key ? a.k_blk : a.v_blk) +
+                               (((size_t)b * a.R + r) * a.Hkv + g) * 128 + 8 * y;
+    float x[4][8];
+#pragma unroll
+    for (int G = 0; G < 4; ++G) load_vec<__nv_bfloat16, 8>(src + 32 * G, x[G]);
+    uint8_t* base = static_cast<uint8_t*>(const_cast<void*>(is_key ? a.k_pages : a.v_pages)) +
+                    ((size_t)(mapped ? page : 0) * a.Hkv + g) * kv4_page_bytes(ps, 128);
+    kv4_store_quad<128>(x, is_key, base, ps, pos % ps, in && mapped);
+  }
+}
+
 // ------------------------------------------------------------------ the kernel
-// 18 warps: two SMSPs host five of them, so a thread may hold at most
-// 16384 / (5 * 32) -> 96 registers.
+// 18 (KV4: 20) warps: an SMSP hosts up to five of them, so a thread may hold at
+// most 16384 / (5 * 32) -> 96 registers.
+template <bool KV4>
 __global__ void __maxnreg__(96)
 attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kp,
                  const __grid_constant__ CUtensorMap tm_vp, const __grid_constant__ CUtensorMap tm_ks,
                  const __grid_constant__ CUtensorMap tm_vs, const Tc05Params prm) {
+  using L = Tc<KV4>;
+  constexpr uint32_t kOffBar = L::kOffBar, kOffMisc = L::kOffMisc, kOffRed = L::kOffRed, kOffOk = L::kOffOk;
+  constexpr int kThreads = L::kThreads, kVStages = L::kVStages, kSoft0 = L::kSoft0;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
   const uint32_t sb = smem_u32(smem);
@@ -151,19 +352,22 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #endif
     for (int i = 0; i < kNumBars; ++i) {
       const bool pfull = i >= BAR_PFULL && i < BAR_PFULL + kStages;
-      mbar_init(sb + kOffBar + 8u * i, pfull ? 8u : 1u);
+      const bool full = i >= BAR_KFULL && i < BAR_KEMPTY;
+      mbar_init(sb + kOffBar + 8u * i, pfull ? 8u : full ? (uint32_t)L::kFull : 1u);
     }
     reinterpret_cast<volatile int*>(smem + kOffMisc)[1] = 0;     // abort flag
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     prefetch_tmap(&tm_q);
-    prefetch_tmap(&tm_kp);
-    prefetch_tmap(&tm_vp);
+    if constexpr (!KV4) {
+      prefetch_tmap(&tm_kp);
+      prefetch_tmap(&tm_vp);
+    }
     prefetch_tmap(&tm_ks);
     prefetch_tmap(&tm_vs);
     const int bq = blockIdx.z / prm.a.Hkv;
     prefetch_l2(prm.a.seq_lens + bq, 4, 0, 1);
-    const int pgq = blockIdx.y * prm.a.keys_per_split / 64;   // the last split may start past the table
+    const int pgq = blockIdx.y * prm.a.keys_per_split / (KV4 ? prm.a.page_size : 64);   // the last split may start past the table
     if (pgq < prm.a.max_pages)
       prefetch_l2(prm.a.page_table + (size_t)bq * prm.a.max_pages + pgq, min(256, 4 * (prm.a.max_pages - pgq)), 0, 1);
   }
@@ -174,7 +378,7 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   // The producer's first two 32-page windows of the page table do not depend on
   // the prefix length, so they load alongside it.
   int win_cur = -1, win_nxt = -1;
-  if (warp == 0) {
+  if (!KV4 && warp == 0) {
     const int32_t* tb = a.page_table + (size_t)b * a.max_pages;
     const int pg = blockIdx.y * a.keys_per_split / 64;
     win_cur = pg + lane < a.max_pages ? tb[pg + lane] : -1;
@@ -199,7 +403,7 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   auto bar = [&](int i) -> uint32_t { return sb + kOffBar + 8u * i; };
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  if (warp == 1) {      // every CTA holds TMEM (released at the end), keys or not
+  if (warp == L::kMma) {      // every CTA holds TMEM (released at the end), keys or not
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + kOffMisc),
                  "r"(kTmemCols)
                  : "memory");
@@ -221,7 +425,9 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   if (bp.nb == 0) {
     // This split holds no prefix keys of sequence b (only possible with
     // nsplit > 1): it contributes an empty partial (lse = -inf) to the merge.
-  } else if (warp == 0) {
+  } else if (KV4 && warp > L::kMma && warp < kSoft0) {
+    if constexpr (KV4) dequantise(prm, tm_q, tm_ks, tm_vs, smem, sb, bp, table, b, g, rho0, abort_flag);
+  } else if (!KV4 && warp == 0) {
     // ---------------------------------------------------------------- producer
     // Separate K and V rings (3 stages each): a K stage is refilled as soon as
     // its S MMA is done, a V stage when its PV is done, so K runs up to three
@@ -338,7 +544,7 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         wait_quiet(bar(BAR_Q), 0);
       }
     }
-  } else if (warp == 1) {
+  } else if (warp == L::kMma) {
     // ---------------------------------------------------------------- MMA issuer
     // Block b belongs to softmax set t = b & 1, which owns S_t and O_t in TMEM.
     // Order: S(0), S(1); then per block b: PV_t(b) and, behind it in the same
@@ -373,8 +579,8 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if (ok) ok = issue_s(0);
       if (ok && bp.nb > 1) ok = issue_s(1);
       for (int b2 = 0; ok && b2 < bp.nb; ++b2) {
-        const int st = b2 % kStages, t = b2 & 1, j = b2 >> 1;
-        if (!wait_bar(bar(BAR_VFULL + st), (uint32_t)((b2 / kStages) & 1), abort_flag, a.err)) break;
+        const int st = b2 % kVStages, t = b2 & 1, j = b2 >> 1;
+        if (!wait_bar(bar(BAR_VFULL + st), (uint32_t)((b2 / kVStages) & 1), abort_flag, a.err)) break;
         if (!wait_bar(bar(BAR_PFULL + t), (uint32_t)(j & 1), abort_flag, a.err)) break;
         fence_after();
         const uint64_t vbase = dv0 + (uint64_t)((st * kTileBytes) >> 4);
@@ -397,19 +603,19 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    // Warps 2..17.  Set t (block parity) = (warp-2)/8 owns S_t and O_t; within a
-    // set, half hf = ((warp-2)/4)&1 takes columns [64hf, 64hf+64) of the rows of
+    // Sixteen warps from kSoft0.  Set t (block parity) = (warp-kSoft0)/8 owns S_t and
+    // O_t; within a set, half hf = ((warp-kSoft0)/4)&1 takes columns [64hf, 64hf+64) of the rows of
     // TMEM lane quarter warp%4.  One thread = one half row.  The two halves of a
     // row swap block maxima at a named barrier (id 1 + 4t + quarter, 64
     // threads); row sums and the two sets are merged in the epilogue.
     const int q4 = warp & 3;
-    const int t = (warp - 2) >> 3;
-    const int hf = ((warp - 2) >> 2) & 1;
+    const int t = (warp - kSoft0) >> 3;
+    const int hf = ((warp - kSoft0) >> 2) & 1;
     const int r = 32 * q4 + lane;
     const int rho_c = min(rho0 + r / a.G, a.R - 1);
     const StepVis vis = step_visibility(a.k, rho_c);
     const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
-    const int gt = (warp - 2 - 8 * t) * 32 + lane;     // 0..255 within the set
+    const int gt = (warp - kSoft0 - 8 * t) * 32 + lane;     // 0..255 within the set
     const bool live = 32 * q4 < rows_valid;             // the warp holds at least one real row
     const float sl2 = prm.scale_log2;
     const int nbt = (bp.nb - t + 1) >> 1;               // blocks of this set
@@ -430,7 +636,8 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int start = bp.k0 + b2 * 128;
         lo_valid = min(64, bp.kend - start);
         hi_valid = max(0, min(64, bp.kend - start - 64));
-        if (lo_valid < 64 || hi_valid < 64) {            // page checks only where a page may be absent
+        // (KV4: keys on an unmapped page were written as zeros)
+        if (!KV4 && (lo_valid < 64 || hi_valid < 64)) {  // page checks only where a page may be absent
           if (!page_ok(table[start / 64], a.num_pages)) lo_valid = 0;
           if (hi_valid > 0 && !page_ok(table[start / 64 + 1], a.num_pages)) hi_valid = 0;
         }
@@ -536,7 +743,7 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
       }
       l = l * f_resc + lblk;
-      if (!window && (lo_valid < 64 || hi_valid < 64)) {
+      if (!KV4 && !window && (lo_valid < 64 || hi_valid < 64)) {
         // keys past the prefix end or on an unmapped page: zero their V rows so
         // that 0 * (whatever the page holds) cannot turn into NaN
         const int st = b2 % kStages;
@@ -620,9 +827,9 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   float* ost = reinterpret_cast<float*>(smem + kOffK);
   float* lst = ost + 128 * kStageStride;
   int* wst = reinterpret_cast<int*>(lst + 128);
-  if (warp >= 2) {
+  if (warp >= kSoft0) {
     const int r = 32 * (warp & 3) + lane;
-    const int t = (warp - 2) >> 3, hf = ((warp - 2) >> 2) & 1;
+    const int t = (warp - kSoft0) >> 3, hf = ((warp - kSoft0) >> 2) & 1;
     if (bp.nb == 0) {
 #pragma unroll
       for (int e = 0; e < 32; ++e) ov[e] = 0.f;
@@ -672,6 +879,9 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // ---------------------------------------------------------------- append
     // Draft rows D_1..D_n of KV head g into cache rows P .. P+n-1 (the keys
     // above read them from k_blk / v_blk, not from the cache).
+    if constexpr (KV4) {
+      append_kv4(a, table, b, g, P);
+    } else
     for (int c = threadIdx.x; c < a.n * 2 * 16; c += kThreads) {
       const int r = c >> 5, which = (c >> 4) & 1, piece = c & 15;
       const int pos = P + r;
@@ -695,7 +905,7 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (trace_cta()) g_tidar_trace[3] = clock64();
 #endif
   }
-  if (warp == 1) {
+  if (warp == L::kMma) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
@@ -703,6 +913,7 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
 // ------------------------------------------------------------------ host side
 // The kernel's dynamic shared memory opt-in, once per device.
+template <bool KV4>
 cudaError_t set_smem_attr() {
   static bool attr_set[64] = {false};
   int dev = 0;
@@ -710,11 +921,84 @@ cudaError_t set_smem_attr() {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorNotSupported;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(attn_tc05_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+    e = cudaFuncSetAttribute(attn_tc05_kernel<KV4>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<KV4>::kSmem);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   return cudaSuccess;
+}
+
+template <bool KV4>
+cudaError_t launch_t(const AttnArgs& a, cudaStream_t s) {
+  if (!a.bf16 || a.D != 128 || (!KV4 && a.page_size != 64) || a.G > 128) return cudaErrorNotSupported;
+  Tc05Params prm;
+  prm.a = a;
+  prm.rho_per_tile = 128 / a.G;
+  prm.tiles = (a.R + prm.rho_per_tile - 1) / prm.rho_per_tile;
+  prm.scale_log2 = a.scale * 1.4426950408889634f;
+  prm.starve = g_starve_loads;
+
+  CUtensorMap tq, tkp, tvp, tks, tvs;
+  {
+    const cuuint64_t dims[4] = {128, (cuuint64_t)a.Hq, (cuuint64_t)a.R, (cuuint64_t)a.B};
+    const cuuint64_t str[3] = {256, (cuuint64_t)a.Hq * 256, (cuuint64_t)a.R * a.Hq * 256};
+    const cuuint32_t box[4] = {64, (cuuint32_t)a.G, (cuuint32_t)prm.rho_per_tile, 1};
+    if (!encode(&tq, a.q, 4, dims, str, box)) return cudaErrorNotSupported;
+  }
+  if constexpr (!KV4) {
+    const cuuint64_t dims[2] = {128, (cuuint64_t)a.num_pages * a.Hkv * 64};
+    const cuuint64_t str[1] = {256};
+    const cuuint32_t box[2] = {64, 64};
+    if (!encode(&tkp, a.k_pages, 2, dims, str, box)) return cudaErrorNotSupported;
+    if (!encode(&tvp, a.v_pages, 2, dims, str, box)) return cudaErrorNotSupported;
+  }
+  {
+    const cuuint64_t dims[4] = {128, (cuuint64_t)a.Hkv, (cuuint64_t)a.R, (cuuint64_t)a.B};
+    const cuuint64_t str[3] = {256, (cuuint64_t)a.Hkv * 256, (cuuint64_t)a.R * a.Hkv * 256};
+    const cuuint32_t box[4] = {64, 1, 128, 1};
+    if (!encode(&tks, a.k_blk, 4, dims, str, box)) return cudaErrorNotSupported;
+    if (!encode(&tvs, a.v_blk, 4, dims, str, box)) return cudaErrorNotSupported;
+  }
+  if constexpr (KV4) tkp = tks, tvp = tvs;              // the kernel reads the pages itself
+  cudaError_t e = set_smem_attr<KV4>();
+  if (e != cudaSuccess) return e;
+  const bool clu = a.nsplit > 1 && a.cluster_merge;
+  if (a.nsplit > 1 && !clu && (!a.part_o || !a.part_lse)) return cudaErrorInvalidValue;
+  if (clu && a.nsplit > kMaxCluster) return cudaErrorNotSupported;
+  const dim3 grid(prm.tiles, a.nsplit, a.B * a.Hkv);
+  // with the cluster merge, the splits of one (b, g, tile) form a cluster
+  const dim3 cluster(1, clu ? a.nsplit : 1, 1);
+  return launch_clustered(attn_tc05_kernel<KV4>, grid, cluster, Tc<KV4>::kThreads, Tc<KV4>::kSmem, s, tq, tkp, tvp, tks,
+                          tvs, prm);
+}
+
+template <bool KV4>
+int resident_clusters_t(int ns) {
+  static int cache[64][kMaxCluster + 1];
+  if (ns < 1 || ns > kMaxCluster) return 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (cache[dev][ns]) return cache[dev][ns] - 1;
+  int n = 0;
+  if (set_smem_attr<KV4>() == cudaSuccess &&
+      (ns <= 8 || cudaFuncSetAttribute(attn_tc05_kernel<KV4>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                      cudaSuccess)) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, ns, 1);
+    cfg.blockDim = dim3(Tc<KV4>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Tc<KV4>::kSmem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 1;
+    at[0].val.clusterDim.y = ns;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, attn_tc05_kernel<KV4>, &cfg) != cudaSuccess) n = 0;
+  }
+  cudaGetLastError();
+  cache[dev][ns] = n + 1;
+  return n;
 }
 
 }  // namespace
@@ -733,73 +1017,9 @@ extern "C" int tidar_trace_clear(void) {
 #endif
 
 cudaError_t launch_attn_tc05(const AttnArgs& a, cudaStream_t s) {
-  if (!a.bf16 || a.D != 128 || a.page_size != 64 || a.G > 128) return cudaErrorNotSupported;
-  Tc05Params prm;
-  prm.a = a;
-  prm.rho_per_tile = 128 / a.G;
-  prm.tiles = (a.R + prm.rho_per_tile - 1) / prm.rho_per_tile;
-  prm.scale_log2 = a.scale * 1.4426950408889634f;
-  prm.starve = g_starve_loads;
-
-  CUtensorMap tq, tkp, tvp, tks, tvs;
-  {
-    const cuuint64_t dims[4] = {128, (cuuint64_t)a.Hq, (cuuint64_t)a.R, (cuuint64_t)a.B};
-    const cuuint64_t str[3] = {256, (cuuint64_t)a.Hq * 256, (cuuint64_t)a.R * a.Hq * 256};
-    const cuuint32_t box[4] = {64, (cuuint32_t)a.G, (cuuint32_t)prm.rho_per_tile, 1};
-    if (!encode(&tq, a.q, 4, dims, str, box)) return cudaErrorNotSupported;
-  }
-  {
-    const cuuint64_t dims[2] = {128, (cuuint64_t)a.num_pages * a.Hkv * 64};
-    const cuuint64_t str[1] = {256};
-    const cuuint32_t box[2] = {64, 64};
-    if (!encode(&tkp, a.k_pages, 2, dims, str, box)) return cudaErrorNotSupported;
-    if (!encode(&tvp, a.v_pages, 2, dims, str, box)) return cudaErrorNotSupported;
-  }
-  {
-    const cuuint64_t dims[4] = {128, (cuuint64_t)a.Hkv, (cuuint64_t)a.R, (cuuint64_t)a.B};
-    const cuuint64_t str[3] = {256, (cuuint64_t)a.Hkv * 256, (cuuint64_t)a.R * a.Hkv * 256};
-    const cuuint32_t box[4] = {64, 1, 128, 1};
-    if (!encode(&tks, a.k_blk, 4, dims, str, box)) return cudaErrorNotSupported;
-    if (!encode(&tvs, a.v_blk, 4, dims, str, box)) return cudaErrorNotSupported;
-  }
-  cudaError_t e = set_smem_attr();
-  if (e != cudaSuccess) return e;
-  const bool clu = a.nsplit > 1 && a.cluster_merge;
-  if (a.nsplit > 1 && !clu && (!a.part_o || !a.part_lse)) return cudaErrorInvalidValue;
-  if (clu && a.nsplit > kMaxCluster) return cudaErrorNotSupported;
-  const dim3 grid(prm.tiles, a.nsplit, a.B * a.Hkv);
-  // with the cluster merge, the splits of one (b, g, tile) form a cluster
-  const dim3 cluster(1, clu ? a.nsplit : 1, 1);
-  return launch_clustered(attn_tc05_kernel, grid, cluster, kThreads, kSmemAlloc, s, tq, tkp, tvp, tks, tvs,
-                          prm);
+  return a.kv4 ? launch_t<true>(a, s) : launch_t<false>(a, s);
 }
 
-int tc05_resident_clusters(int ns) {
-  static int cache[64][kMaxCluster + 1];
-  if (ns < 1 || ns > kMaxCluster) return 0;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (cache[dev][ns]) return cache[dev][ns] - 1;
-  int n = 0;
-  if (set_smem_attr() == cudaSuccess &&
-      (ns <= 8 || cudaFuncSetAttribute(attn_tc05_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
-                      cudaSuccess)) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(1, ns, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmemAlloc;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 1;
-    at[0].val.clusterDim.y = ns;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, attn_tc05_kernel, &cfg) != cudaSuccess) n = 0;
-  }
-  cudaGetLastError();
-  cache[dev][ns] = n + 1;
-  return n;
-}
+int tc05_resident_clusters(int ns, bool kv4) { return kv4 ? resident_clusters_t<true>(ns) : resident_clusters_t<false>(ns); }
 
 }  // namespace tidar

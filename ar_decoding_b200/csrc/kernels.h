@@ -45,7 +45,7 @@ cudaError_t launch_attn_kv4_dec(const AttnArgs& a, cudaStream_t s);
 int kv4_dec_resident_clusters(int ns, int M);
 // CUDA-core kernel (fp32 or bf16, D 64 or 128; either cache).
 cudaError_t launch_attn_simt(const AttnArgs& a, cudaStream_t s);
-// tcgen05/TMEM kernel (bf16, D 128, page 64).  Returns cudaErrorNotSupported if
+// tcgen05/TMEM kernel (bf16, D 128, page 64; kv4: any page size).  Returns cudaErrorNotSupported if
 // the tensor maps cannot be built.
 cudaError_t launch_attn_tc05(const AttnArgs& a, cudaStream_t s);
 // How many clusters of `ns` tcgen05 attention CTAs (one per key split) this
@@ -53,7 +53,7 @@ cudaError_t launch_attn_tc05(const AttnArgs& a, cudaStream_t s);
 // cluster and merge over distributed shared memory (and the kernel performs
 // the draft-row append), else they write part_o / part_lse and
 // launch_finalize merges and appends.
-int tc05_resident_clusters(int ns);
+int tc05_resident_clusters(int ns, bool kv4);
 // Tensor-core kernel with two 128-row query tiles per CTA sharing each staged
 // K/V block (bf16, D 128, page 64), for query blocks of more than one tile per
 // KV head.  Split merge and append as launch_attn_tc05.
