@@ -19,6 +19,7 @@
 //     word per group, each pair becomes 136 + c, minus 136, times the two keys'
 //     scales (exact in bf16; the sums run over the whole prefix here, so an
 //     offset in the accumulator would cost its low bits).
+// The integer pipe (shifts, masks, permutes: half the issue rate) bounds it.
 // Both products are exact up to the fp32 accumulation, so the only rounding
 // besides it is p's to bf16.  MMA row r of a 16-key block is physical key
 // (r % 8) / 2 + 4 (r % 2) + 8 (r / 8): the four keys whose values a lane loads
@@ -94,15 +95,6 @@ __device__ __forceinline__ void mma16816_c(float (&d)[4], uint32_t a0, uint32_t 
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
-// Pair i of a word of codes as the bf16 numbers 136 + c: one shift and one
-// three-input logic instruction, (x & 0x000f000f) ^ 0x43084308 (left to the
-// compiler, the two constants cost two instructions; the integer pipe, at half
-// the issue rate, is what bounds this kernel).
-__device__ __forceinline__ uint32_t offset_codes(uint32_t w, int i) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(0x43084308u));
   return r;
 }
 __device__ __forceinline__ uint32_t sub136_mul(uint32_t x, uint32_t s) {
@@ -406,7 +398,7 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
         for (int G = 0; G < 4; ++G) {
           uint32_t ra[4], rd[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) ra[e] = offset_codes(wa[G], e), rd[e] = offset_codes(wd[G], e);
+          for (int e = 0; e < 4; ++e) ra[e] = kv4_offset_codes(wa[G], e), rd[e] = kv4_offset_codes(wd[G], e);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float acc[4];
@@ -458,7 +450,7 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
             const uint32_t w = G < 2 ? __byte_perm(c[2 * pr].x, c[2 * pr + 1].x, sel) : __byte_perm(c[2 * pr].y, c[2 * pr + 1].y, sel);
             const uint32_t sp = G < 2 ? __byte_perm(t[2 * pr].x, t[2 * pr + 1].x, sel) : __byte_perm(t[2 * pr].y, t[2 * pr + 1].y, sel);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[pr][e] = sub136_mul(offset_codes(w, e), sp);
+            for (int e = 0; e < 4; ++e) v[pr][e] = sub136_mul(kv4_offset_codes(w, e), sp);
           }
 #pragma unroll
           for (int j = 0; j < 2; ++j)

@@ -38,8 +38,8 @@
 // memory), or write fp32 partials to the workspace for a finalize launch.
 // KV4 (the 4-bit cache of kv4.cuh, any page size): 20 warps.  Warp 0 is the MMA
 // issuer, warps 1..3 take the producer's place for prefix blocks: they copy
-// codes and scales in groups of 8 keys (asynchronous copies, twelve groups
-// ahead each), turn them into the bf16 values they stand for (exact) and write
+// codes and scales in groups of 8 keys (asynchronous copies, three phases --
+// blocks of one operand -- ahead), turn them into the bf16 values they stand for (exact) and write
 // those into the K and V rings in the layout that TMA would have left, in the
 // order K0, K1, V0, K2, V1, ..; warps 4..19 are the softmax warps.  Step-key
 // windows still come by TMA.  A V ring of two stages makes room for the raw
@@ -76,9 +76,11 @@ constexpr int kNumBars = 23;
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = kOffQ + kTileBytes;
 constexpr uint32_t kOffV = kOffK + kStages * kTileBytes;
-// KV4: dequantising warps, and each one's ring of raw groups of 8 keys
+// KV4: dequantising warps, and each one's ring of raw groups of 8 keys: a phase
+// is one block of one operand, 16 groups, at most 6 of them a warp's
 constexpr int kDqWarps = 3;
-constexpr int kRawDepth = 12;
+constexpr int kRawPhases = 3;
+constexpr int kRawPer = 6;
 constexpr uint32_t kRawGroup = 8 * 72;                  // codes, then scales
 // Warp roles and the shared-memory layout behind the rings.
 template <bool KV4> struct Tc {
@@ -88,7 +90,7 @@ template <bool KV4> struct Tc {
   static constexpr int kVStages = KV4 ? 2 : kStages;
   static constexpr int kFull = KV4 ? kDqWarps : 1;      // arrivals that fill a stage
   static constexpr uint32_t kOffRaw = kOffV + kVStages * kTileBytes;
-  static constexpr uint32_t kOffBar = kOffRaw + (KV4 ? kDqWarps * kRawDepth * kRawGroup : 0);
+  static constexpr uint32_t kOffBar = kOffRaw + (KV4 ? kDqWarps * kRawPhases * kRawPer * kRawGroup : 0);
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;   // [0] TMEM base, [1] abort flag
   static constexpr uint32_t kOffRed = kOffMisc + 16;             // softmax halves: maxima [2][2][128] f32
   static constexpr uint32_t kOffOk = kOffRed + 2048;             // and warp status [2][2][4] i32
@@ -150,8 +152,7 @@ static_assert((128 * kStageStride + 256) * 4 <= kStages * kTileBytes, "row stagi
 // chunk y of key kk: eight dims of each of the four groups of 32, 16 bytes of
 // bf16 each.  Eight lanes then hold keys k and k + 4, whose swizzled 16-byte
 // units fall into different halves of the 128-byte row: stores without bank
-// conflicts.  Twelve groups (6.9 KB) a warp in flight; converting a block of
-// 128 keys is 32 groups of about 85 instructions over the three warps.
+// conflicts.  Warp w takes groups (w + p) % 3, + 3, .. of phase p.
 __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensorMap& tm_q, const CUtensorMap& tm_ks,
                                            const CUtensorMap& tm_vs, uint8_t* smem, uint32_t sb, const BlockPlan& bp,
                                            const int32_t* table, int b, int g, int rho0, volatile int* abort_flag) {
@@ -169,73 +170,77 @@ __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensor
   const uint8_t* kbase = static_cast<const uint8_t*>(a.k_pages) + (size_t)g * page_bytes;
   const uint8_t* vbase = static_cast<const uint8_t*>(a.v_pages) + (size_t)g * page_bytes;
   const int kk = ((lane >> 3) & 3) + 4 * ((lane >> 2) & 1), y = lane & 3;
-  const uint32_t raw0 = L::kOffRaw + (uint32_t)w * (kRawDepth * kRawGroup);
+  const uint32_t raw0 = L::kOffRaw + (uint32_t)w * (kRawPhases * kRawPer * kRawGroup);
   // Phase p of the conversion: K(0); then for j = 1, 2, ..: K(j) at 2j - 1 and
   // V(j - 1) at 2j, up to V(nb - 1).  Block of phase p, -1 for K past the last.
   const int phases = 2 * bp.nb + 1;
   auto block_of = [&](int p) -> int { return p == 0 ? 0 : (p & 1) ? ((p + 1) / 2 < bp.nb ? (p + 1) / 2 : -1) : p / 2 - 1; };
   auto is_v = [&](int p) -> bool { return p > 0 && !(p & 1); };
-  auto has_groups = [&](int p) -> bool { const int i = block_of(p); return i >= 0 && i < bp.npb; };
-  // The copies run ahead along the same sequence of (phase, group): this warp's
-  // groups of phase p are (w + p) % 3, + 3, ..
   bool bad = false;
-  uint32_t slot_ok = 0;
-  int ip = 0, ig = w, slot_i = 0, pg_next = -1;
-  auto settle = [&]() {           // moves the copy iterator to a phase that has groups
-    while (ip < phases && (!has_groups(ip) || ig >= 16)) {
-      ++ip;
-      ig = (w + ip) % 3;
-    }
-  };
-  auto load_page = [&]() -> int { // page of the copy iterator's group (-1: none)
-    if (ip >= phases) return -1;
-    const int key = bp.k0 + 128 * block_of(ip) + 8 * ig;
+  // Table entry of group `lane` (16 of them) of phase p: -1 where it has no key
+  // or no valid page.  Loaded a phase before its copies are queued.
+  auto load_entries = [&](int p) -> int {
+    const int i = p < phases ? block_of(p) : -1;
+    if (i < 0 || i >= bp.npb) return -1;
+    const int key = bp.k0 + 128 * i + 8 * (lane & 15);
     if (key >= bp.kend) return -1;
     const int pg = table[key >> lps];
     if (page_ok(pg, a.num_pages)) return pg;
     bad = true;
     return -1;
   };
-  auto copy_one = [&]() {
-    if (ip < phases) {
-      const int key = bp.k0 + 128 * block_of(ip) + 8 * ig, pg = pg_next;
-      if (pg >= 0) {
-        const int row = key & (ps - 1);
-        const uint8_t* base = (is_v(ip) ? vbase : kbase) + (size_t)pg * page_stride;
-        const uint32_t dst = sb + raw0 + (uint32_t)slot_i * kRawGroup;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16u * lane), "l"(base + (size_t)row * 64 + kk * 64 + y * 16)
-                     : "memory");
-        if (lane < 4)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512u + 16u * lane),
-                       "l"(base + (size_t)ps * 64 + (size_t)row * 8 + 16 * lane)
+  const uint32_t own = (uint32_t)(kk * 64 + y * 16);
+  const uint32_t scale_off = (uint32_t)ps * 64u + 16u * lane;
+  // Queues this warp's copies of phase p into raw slot p % kRawPhases (always
+  // one commit group).
+  auto copy_phase = [&](int p, int entries) {
+    const int i = p < phases ? block_of(p) : -1;
+    if (i >= 0 && i < bp.npb) {
+      const uint8_t* base = is_v(p) ? vbase : kbase;
+      const int q0 = (w + p) % 3;
+      const uint32_t dst = sb + raw0 + (uint32_t)(p % kRawPhases) * (kRawPer * kRawGroup) + 16u * lane;
+#pragma unroll
+      for (int j = 0; j < kRawPer; ++j) {
+        const int q = q0 + 3 * j;
+        const int pg = __shfl_sync(0xffffffffu, entries, q & 15);
+        if (q < 16 && pg >= 0) {
+          const uint32_t row = (uint32_t)(bp.k0 + 128 * i + 8 * q) & (uint32_t)(ps - 1);
+          const uint8_t* src = base + (size_t)pg * page_stride;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * kRawGroup), "l"(src + row * 64 + own)
                        : "memory");
+          if (lane < 4)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * kRawGroup + 512u),
+                         "l"(src + scale_off + row * 8)
+                         : "memory");
+        }
       }
-      // one bit a slot: the group lies on a valid page
-      slot_ok = (slot_ok & ~(1u << slot_i)) | ((pg >= 0 ? 1u : 0u) << slot_i);
-      ig += 3;
-      settle();
-      pg_next = load_page();
-      if (++slot_i == kRawDepth) slot_i = 0;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  settle();
-  pg_next = load_page();
-  if (!prm.starve)
-    for (int i = 0; i < kRawDepth - 1; ++i) copy_one();
-
-  int slot = 0;
+  // groups of the next three phases that lie on a valid page
+  uint32_t live0 = 0, live1 = 0, live2 = 0;
+  int entries = load_entries(0);
+  auto advance = [&](int p) {                              // queue phase p, look up phase p + 1
+    live0 = live1;
+    live1 = live2;
+    live2 = __ballot_sync(0xffffffffu, entries >= 0);
+    copy_phase(p, entries);
+    entries = load_entries(p + 1);
+  };
   bool ok = !prm.starve;
+  if (ok)
+    for (int p = 0; p < kRawPhases; ++p) advance(p);
   for (int p = 0; ok && p < phases; ++p) {
     const int i = block_of(p);
-    if (i < 0) continue;
     const bool v = is_v(p);
     const int ns = v ? L::kVStages : kStages, s = i % ns;
     const uint32_t full = bar((v ? BAR_VFULL : BAR_KFULL) + s);
     if (i >= ns) ok = warp_wait_bar(bar((v ? BAR_VEMPTY : BAR_KEMPTY) + s), (uint32_t)((i / ns - 1) & 1), abort_flag, a.err);
     if (!ok) break;
     const uint32_t tile = (v ? kOffV : kOffK) + (uint32_t)s * kTileBytes;
-    if (i >= bp.npb) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRawPhases - 1) : "memory");
+    __syncwarp();
+    if (i >= bp.npb) {                                     // a step-key window
       if (lane == 0) {
         if (w == 0) {
           const CUtensorMap* map = v ? &tm_vs : &tm_ks;
@@ -247,44 +252,42 @@ __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensor
           mbar_arrive(full);
         }
       }
-      __syncwarp();
-      continue;
-    }
-    for (int q = (w + p) % 3; q < 16; q += 3) {
-      copy_one();                                          // refills the slot that the last group left
-      asm volatile("cp.async.wait_group %0;" ::"n"(kRawDepth - 1) : "memory");
-      __syncwarp();
-      const uint8_t* raw = smem + raw0 + (uint32_t)slot * kRawGroup;
-      const int key = 8 * q + kk;
-      uint4 c = *reinterpret_cast<const uint4*>(raw + 16 * lane);
-      uint2 sc = *reinterpret_cast<const uint2*>(raw + 512 + 8 * kk);
-      const bool live = ((slot_ok >> slot) & 1u) && bp.k0 + 128 * i + key < bp.kend;
-      if (!live) c = make_uint4(0, 0, 0, 0), sc = make_uint2(0, 0);
-      uint32_t words[4] = {c.x, c.y, c.z, c.w};
-      if (v) {
-        const uint32_t raw4[4] = {c.x, c.y, c.z, c.w};
-        kv4_value_to_key<4>(raw4, words);
-      }
-      const uint32_t sp[4] = {__byte_perm(sc.x, 0, 0x1010), __byte_perm(sc.x, 0, 0x3232), __byte_perm(sc.y, 0, 0x1010),
-                              __byte_perm(sc.y, 0, 0x3232)};
-      uint8_t* row = smem + tile + key * 128;
+    } else if (i >= 0) {
+      const uint8_t* raw = smem + raw0 + (uint32_t)(p % kRawPhases) * (kRawPer * kRawGroup);
+      const int q0 = (w + p) % 3, left = bp.kend - bp.k0 - 128 * i;      // keys of the block that exist
 #pragma unroll
-      for (int G = 0; G < 4; ++G) {
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 x = __hmul2(kv4_codes2(words[G], e), *reinterpret_cast<const __nv_bfloat162*>(&sp[G]));
-          o[e] = *reinterpret_cast<const uint32_t*>(&x);
+      for (int j = 0; j < kRawPer; ++j) {
+        const int q = q0 + 3 * j, key = 8 * q + kk;
+        if (q >= 16) break;
+        uint4 c = *reinterpret_cast<const uint4*>(raw + j * kRawGroup + 16 * lane);
+        uint2 sc = *reinterpret_cast<const uint2*>(raw + j * kRawGroup + 512 + 8 * kk);
+        if (key >= left || !((live0 >> q) & 1u)) c = make_uint4(0, 0, 0, 0), sc = make_uint2(0, 0);
+        uint32_t words[4] = {c.x, c.y, c.z, c.w};
+        if (v) {
+          const uint32_t raw4[4] = {c.x, c.y, c.z, c.w};
+          kv4_value_to_key<4>(raw4, words);
         }
-        *reinterpret_cast<uint4*>(row + (G >> 1) * kChunkBytes + (((4 * (G & 1) + y) ^ (key & 7)) << 4)) =
-            make_uint4(o[0], o[1], o[2], o[3]);
+        const uint32_t sp[4] = {__byte_perm(sc.x, 0, 0x1010), __byte_perm(sc.x, 0, 0x3232),
+                                __byte_perm(sc.y, 0, 0x1010), __byte_perm(sc.y, 0, 0x3232)};
+        uint8_t* row = smem + tile + key * 128;
+#pragma unroll
+        for (int G = 0; G < 4; ++G) {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 x = __hmul2(kv4_codes2(words[G], e), *reinterpret_cast<const __nv_bfloat162*>(&sp[G]));
+            o[e] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          *reinterpret_cast<uint4*>(row + (G >> 1) * kChunkBytes + (((4 * (G & 1) + y) ^ (key & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+        }
       }
-      __syncwarp();                                        // every lane has read the slot's scales
-      if (++slot == kRawDepth) slot = 0;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full);
     }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) mbar_arrive(full);
+    __syncwarp();                                          // every lane has read the raw slot: refill it
+    advance(p + kRawPhases);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (bad) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);

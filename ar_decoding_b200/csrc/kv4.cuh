@@ -89,11 +89,18 @@ __device__ __forceinline__ void kv4_value_to_key(const uint32_t (&v)[N], uint32_
   }
 }
 
-// Pair i of a key-row word (dims 2i, 2i+1 of its eight), as bf16 codes: the
-// nibbles, offset by 8, become the low mantissa bits of 128, and 136 is taken
-// off again.
+// Pair i of a key-row word (dims 2i, 2i+1 of its eight) as the bf16 numbers
+// 136 + c: the nibbles, offset by 8, become the low mantissa bits of 128.  One
+// shift and one three-input logic instruction, (x & 0x000f000f) ^ 0x43084308
+// (left to the compiler, the two constants cost two instructions).
+__device__ __forceinline__ uint32_t kv4_offset_codes(uint32_t w, int i) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(0x43084308u));
+  return r;
+}
+// The same pair as the codes themselves.
 __device__ __forceinline__ __nv_bfloat162 kv4_codes2(uint32_t w, int i) {
-  const uint32_t b = ((w >> (4 * i)) & 0x000f000fu) ^ 0x43084308u;
+  const uint32_t b = kv4_offset_codes(w, i);
   return __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), __float2bfloat162_rn(136.f));
 }
 
