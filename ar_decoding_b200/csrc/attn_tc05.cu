@@ -36,14 +36,13 @@
 // merge in this kernel (cluster_merge: each CTA stages its normalised rows in
 // shared memory and owners read their peers' rows over distributed shared
 // memory), or write fp32 partials to the workspace for a finalize launch.
-// KV4 (the 4-bit cache of kv4.cuh, any page size): 20 warps.  Warp 0 is the MMA
-// issuer, warps 1..3 take the producer's place for prefix blocks: they copy
-// codes and scales in groups of 8 keys (asynchronous copies, three phases --
-// blocks of one operand -- ahead), turn them into the bf16 values they stand for (exact) and write
-// those into the K and V rings in the layout that TMA would have left, in the
-// order K0, K1, V0, K2, V1, ..; warps 4..19 are the softmax warps.  Step-key
-// windows still come by TMA.  A V ring of two stages makes room for the raw
-// groups.  With 20 warps every thread may hold 96 registers, as in the bf16 form.
+// KV4 (the 4-bit cache of kv4.cuh, any page size): 24 warps.  Warp 0 is the MMA
+// issuer, warps 1..7 take the producer's place for prefix blocks: they copy
+// codes and scales in groups of 8 keys (asynchronous copies, two turns ahead),
+// turn them into the bf16 values they stand for (exact) and write those into the
+// K and V rings in the layout that TMA would have left, in the order K0, K1, V0,
+// K2, V1, ..; warps 8..23 are the softmax warps.  Step-key windows still come by
+// TMA.  Rings of two stages make room for the raw groups.
 // Every mbarrier wait is bounded: on expiry the CTA records TIDAR_DEVERR_TIMEOUT,
 // stops issuing, drains what it issued (bounded), frees TMEM and exits.
 #include <cuda.h>
@@ -59,7 +58,7 @@ namespace tidar {
 
 namespace {
 
-constexpr int kStages = 3;       // K ring depth
+constexpr int kStages = 3;       // bf16: K and V ring depth; S buffers
 constexpr uint32_t kChunkBytes = 16384;                 // 128 rows x 128 B (64 bf16)
 constexpr uint32_t kTileBytes = 2 * kChunkBytes;        // 128 x 128 bf16
 // barrier indices
@@ -75,22 +74,24 @@ constexpr int BAR_VEMPTY = 20;   // + stage: V stage free again (its PV MMA is d
 constexpr int kNumBars = 23;
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = kOffQ + kTileBytes;
-constexpr uint32_t kOffV = kOffK + kStages * kTileBytes;
-// KV4: dequantising warps, and each one's ring of raw groups of 8 keys: a phase
-// is one block of one operand, 16 groups, at most 6 of them a warp's
-constexpr int kDqWarps = 3;
-constexpr int kRawPhases = 3;
-constexpr int kRawPer = 6;
+// KV4: dequantising warps.  A block of one operand is 16 groups of 8 keys, two
+// or three of them a warp's; a turn converts a K and a V block, and the raw
+// copies run two turns ahead.
+constexpr int kDqWarps = 7;
+constexpr int kRawTurns = 2;
+constexpr int kRawPer = 3;
 constexpr uint32_t kRawGroup = 8 * 72;                  // codes, then scales
+constexpr uint32_t kRawTurn = 2 * kRawPer * kRawGroup;  // K groups, then V groups
 // Warp roles and the shared-memory layout behind the rings.
 template <bool KV4> struct Tc {
-  static constexpr int kThreads = KV4 ? 640 : 576;
+  static constexpr int kThreads = KV4 ? 768 : 576;
   static constexpr int kMma = KV4 ? 0 : 1;              // MMA issuer and TMEM owner
   static constexpr int kSoft0 = KV4 ? 1 + kDqWarps : 2; // first of the 16 softmax warps
-  static constexpr int kVStages = KV4 ? 2 : kStages;
+  static constexpr int kRing = KV4 ? 2 : kStages;       // K and V ring depth
   static constexpr int kFull = KV4 ? kDqWarps : 1;      // arrivals that fill a stage
-  static constexpr uint32_t kOffRaw = kOffV + kVStages * kTileBytes;
-  static constexpr uint32_t kOffBar = kOffRaw + (KV4 ? kDqWarps * kRawPhases * kRawPer * kRawGroup : 0);
+  static constexpr uint32_t kOffV = kOffK + kRing * kTileBytes;
+  static constexpr uint32_t kOffRaw = kOffV + kRing * kTileBytes;
+  static constexpr uint32_t kOffBar = kOffRaw + (KV4 ? kDqWarps * kRawTurns * kRawTurn : 0);
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;   // [0] TMEM base, [1] abort flag
   static constexpr uint32_t kOffRed = kOffMisc + 16;             // softmax halves: maxima [2][2][128] f32
   static constexpr uint32_t kOffOk = kOffRed + 2048;             // and warp status [2][2][4] i32
@@ -143,7 +144,19 @@ __device__ __forceinline__ bool trace_cta() { return blockIdx.x == 0 && blockIdx
 #endif
 
 using namespace tc05;
-static_assert((128 * kStageStride + 256) * 4 <= kStages * kTileBytes, "row staging fits the K ring");
+static_assert((128 * kStageStride + 256) * 4 <= Tc<true>::kRing * kTileBytes + Tc<true>::kRing * kTileBytes, "row staging fits the rings");
+
+// 64 score columns: one TMEM load, or two of 32 columns where the launch's 80
+// registers a thread do not hold the wide one's operands (KV4).
+template <bool KV4>
+__device__ __forceinline__ void ld_half_row(uint32_t taddr, uint32_t (&x)[64]) {
+  if constexpr (KV4) {
+    tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+    tmem_ld32(taddr + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+  } else {
+    tmem_ld64(taddr, x);
+  }
+}
 
 // ------------------------------------------------------------------ 4-bit cache
 // The dequantising warps (1 .. kDqWarps) of a KV4 CTA: Q, then the blocks of
@@ -152,7 +165,9 @@ static_assert((128 * kStageStride + 256) * 4 <= kStages * kTileBytes, "row stagi
 // chunk y of key kk: eight dims of each of the four groups of 32, 16 bytes of
 // bf16 each.  Eight lanes then hold keys k and k + 4, whose swizzled 16-byte
 // units fall into different halves of the 128-byte row: stores without bank
-// conflicts.  Warp w takes groups (w + p) % 3, + 3, .. of phase p.
+// conflicts.  Warp w takes groups (w + i) % 7, + 7, .. of block i.  What a warp spends on
+// control (page ids, addresses, waits) is of the order of its conversions, so a
+// turn takes a K and a V block together.
 __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensorMap& tm_q, const CUtensorMap& tm_ks,
                                            const CUtensorMap& tm_vs, uint8_t* smem, uint32_t sb, const BlockPlan& bp,
                                            const int32_t* table, int b, int g, int rho0, volatile int* abort_flag) {
@@ -170,134 +185,143 @@ __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensor
   const uint8_t* kbase = static_cast<const uint8_t*>(a.k_pages) + (size_t)g * page_bytes;
   const uint8_t* vbase = static_cast<const uint8_t*>(a.v_pages) + (size_t)g * page_bytes;
   const int kk = ((lane >> 3) & 3) + 4 * ((lane >> 2) & 1), y = lane & 3;
-  const uint32_t raw0 = L::kOffRaw + (uint32_t)w * (kRawPhases * kRawPer * kRawGroup);
-  // Phase p of the conversion: K(0); then for j = 1, 2, ..: K(j) at 2j - 1 and
-  // V(j - 1) at 2j, up to V(nb - 1).  Block of phase p, -1 for K past the last.
-  const int phases = 2 * bp.nb + 1;
-  auto block_of = [&](int p) -> int { return p == 0 ? 0 : (p & 1) ? ((p + 1) / 2 < bp.nb ? (p + 1) / 2 : -1) : p / 2 - 1; };
-  auto is_v = [&](int p) -> bool { return p > 0 && !(p & 1); };
+  const uint32_t stride32 = (uint32_t)page_stride;       // below 2^32: 65535 heads at most
+  const uint32_t raw0 = L::kOffRaw + (uint32_t)w * (kRawTurns * kRawTurn);
+  const uint32_t own = (uint32_t)(kk * 64 + y * 16), scale_off = (uint32_t)ps * 64u + 16u * lane;
   bool bad = false;
-  // Table entry of group `lane` (16 of them) of phase p: -1 where it has no key
-  // or no valid page.  Loaded a phase before its copies are queued.
-  auto load_entries = [&](int p) -> int {
-    const int i = p < phases ? block_of(p) : -1;
-    if (i < 0 || i >= bp.npb) return -1;
+  // Table entry of group `lane` (16 of them) of prefix block i: -1 where there
+  // is no key or no valid page.
+  auto load_entries = [&](int i) -> int {
     const int key = bp.k0 + 128 * i + 8 * (lane & 15);
-    if (key >= bp.kend) return -1;
+    if (i >= bp.npb || key >= bp.kend) return -1;
     const int pg = table[key >> lps];
     if (page_ok(pg, a.num_pages)) return pg;
     bad = true;
     return -1;
   };
-  const uint32_t own = (uint32_t)(kk * 64 + y * 16);
-  const uint32_t scale_off = (uint32_t)ps * 64u + 16u * lane;
-  // Queues this warp's copies of phase p into raw slot p % kRawPhases (always
-  // one commit group).
-  auto copy_phase = [&](int p, int entries) {
-    const int i = p < phases ? block_of(p) : -1;
-    if (i >= 0 && i < bp.npb) {
-      const uint8_t* base = is_v(p) ? vbase : kbase;
-      const int q0 = (w + p) % 3;
-      const uint32_t dst = sb + raw0 + (uint32_t)(p % kRawPhases) * (kRawPer * kRawGroup) + 16u * lane;
+  // This warp's groups of block i: (w + i) % 7, + 7, + 14 (below 16).
+  auto first_group = [&](int i) -> int { return (w + i) % kDqWarps; };
+  auto copy_block = [&](const uint8_t* base, uint32_t dst, int i, int entries) {
+    const int q0 = first_group(i);
 #pragma unroll
-      for (int j = 0; j < kRawPer; ++j) {
-        const int q = q0 + 3 * j;
-        const int pg = __shfl_sync(0xffffffffu, entries, q & 15);
-        if (q < 16 && pg >= 0) {
-          const uint32_t row = (uint32_t)(bp.k0 + 128 * i + 8 * q) & (uint32_t)(ps - 1);
-          const uint8_t* src = base + (size_t)pg * page_stride;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * kRawGroup), "l"(src + row * 64 + own)
+    for (int j = 0; j < kRawPer; ++j) {
+      const int q = q0 + kDqWarps * j;
+      const int pg = __shfl_sync(0xffffffffu, entries, q & 15);
+      if (q < 16 && pg >= 0) {
+        const uint32_t row = (uint32_t)(bp.k0 + 128 * i + 8 * q) & (uint32_t)(ps - 1);
+        const uint8_t* src = base + (uint64_t)(uint32_t)pg * stride32;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * kRawGroup), "l"(src + (row * 64 + own))
+                     : "memory");
+        if (lane < 4)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * kRawGroup + 512u),
+                       "l"(src + (scale_off + row * 8))
                        : "memory");
-          if (lane < 4)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * kRawGroup + 512u),
-                         "l"(src + scale_off + row * 8)
-                         : "memory");
-        }
       }
     }
+  };
+  // Turn j converts K(j) and V(j - 1).  Its copies (one commit group) go into
+  // raw slot j % 2; e_k, e_v are the table entries of blocks j and j - 1.
+  auto copy_turn = [&](int j, int e_k, int e_v) {
+    const uint32_t dst = sb + raw0 + (uint32_t)(j & 1) * kRawTurn + 16u * lane;
+    if (j < bp.npb) copy_block(kbase, dst, j, e_k);
+    if (j >= 1 && j <= bp.npb) copy_block(vbase, dst + kRawPer * kRawGroup, j - 1, e_v);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // groups of the next three phases that lie on a valid page
-  uint32_t live0 = 0, live1 = 0, live2 = 0;
-  int entries = load_entries(0);
-  auto advance = [&](int p) {                              // queue phase p, look up phase p + 1
-    live0 = live1;
-    live1 = live2;
-    live2 = __ballot_sync(0xffffffffu, entries >= 0);
-    copy_phase(p, entries);
-    entries = load_entries(p + 1);
+  // Converts this warp's groups of block i from `raw` into the ring tile.
+  auto convert = [&](auto is_v, const uint8_t* raw, uint32_t tile, int i, uint32_t live) {
+    const int q0 = first_group(i), left = bp.kend - bp.k0 - 128 * i;      // keys of the block that exist
+#pragma unroll
+    for (int j = 0; j < kRawPer; ++j) {
+      const int q = q0 + kDqWarps * j, key = 8 * q + kk;
+      if (q >= 16) break;
+      uint4 c = *reinterpret_cast<const uint4*>(raw + j * kRawGroup + 16 * lane);
+      uint2 sc = *reinterpret_cast<const uint2*>(raw + j * kRawGroup + 512 + 8 * kk);
+      if (key >= left || !((live >> q) & 1u)) c = make_uint4(0, 0, 0, 0), sc = make_uint2(0, 0);
+      uint32_t words[4] = {c.x, c.y, c.z, c.w};
+      if constexpr (decltype(is_v)::value) {
+        const uint32_t raw4[4] = {c.x, c.y, c.z, c.w};
+        kv4_value_to_key<4>(raw4, words);
+      }
+      const uint32_t sp[4] = {__byte_perm(sc.x, 0, 0x1010), __byte_perm(sc.x, 0, 0x3232),
+                              __byte_perm(sc.y, 0, 0x1010), __byte_perm(sc.y, 0, 0x3232)};
+      uint8_t* row = smem + tile + key * 128;
+#pragma unroll
+      for (int G = 0; G < 4; ++G) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 x = __hmul2(kv4_codes2(words[G], e), *reinterpret_cast<const __nv_bfloat162*>(&sp[G]));
+          o[e] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+        *reinterpret_cast<uint4*>(row + (G >> 1) * kChunkBytes + (((4 * (G & 1) + y) ^ (key & 7)) << 4)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   };
-  bool ok = !prm.starve;
-  if (ok)
-    for (int p = 0; p < kRawPhases; ++p) advance(p);
-  for (int p = 0; ok && p < phases; ++p) {
-    const int i = block_of(p);
-    const bool v = is_v(p);
-    const int ns = v ? L::kVStages : kStages, s = i % ns;
-    const uint32_t full = bar((v ? BAR_VFULL : BAR_KFULL) + s);
-    if (i >= ns) ok = warp_wait_bar(bar((v ? BAR_VEMPTY : BAR_KEMPTY) + s), (uint32_t)((i / ns - 1) & 1), abort_flag, a.err);
-    if (!ok) break;
-    const uint32_t tile = (v ? kOffV : kOffK) + (uint32_t)s * kTileBytes;
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRawPhases - 1) : "memory");
-    __syncwarp();
-    if (i >= bp.npb) {                                     // a step-key window
-      if (lane == 0) {
-        if (w == 0) {
-          const CUtensorMap* map = v ? &tm_vs : &tm_ks;
-          const int win = bp.wins[i - bp.npb];
-          mbar_expect_tx(full, kTileBytes);
-          tma_load_4d(sb + tile, map, 0, g, win * 128, b, full);
-          tma_load_4d(sb + tile + kChunkBytes, map, 64, g, win * 128, b, full);
-        } else {
-          mbar_arrive(full);
-        }
-      }
-    } else if (i >= 0) {
-      const uint8_t* raw = smem + raw0 + (uint32_t)(p % kRawPhases) * (kRawPer * kRawGroup);
-      const int q0 = (w + p) % 3, left = bp.kend - bp.k0 - 128 * i;      // keys of the block that exist
-#pragma unroll
-      for (int j = 0; j < kRawPer; ++j) {
-        const int q = q0 + 3 * j, key = 8 * q + kk;
-        if (q >= 16) break;
-        uint4 c = *reinterpret_cast<const uint4*>(raw + j * kRawGroup + 16 * lane);
-        uint2 sc = *reinterpret_cast<const uint2*>(raw + j * kRawGroup + 512 + 8 * kk);
-        if (key >= left || !((live0 >> q) & 1u)) c = make_uint4(0, 0, 0, 0), sc = make_uint2(0, 0);
-        uint32_t words[4] = {c.x, c.y, c.z, c.w};
-        if (v) {
-          const uint32_t raw4[4] = {c.x, c.y, c.z, c.w};
-          kv4_value_to_key<4>(raw4, words);
-        }
-        const uint32_t sp[4] = {__byte_perm(sc.x, 0, 0x1010), __byte_perm(sc.x, 0, 0x3232),
-                                __byte_perm(sc.y, 0, 0x1010), __byte_perm(sc.y, 0, 0x3232)};
-        uint8_t* row = smem + tile + key * 128;
-#pragma unroll
-        for (int G = 0; G < 4; ++G) {
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 x = __hmul2(kv4_codes2(words[G], e), *reinterpret_cast<const __nv_bfloat162*>(&sp[G]));
-            o[e] = *reinterpret_cast<const uint32_t*>(&x);
-          }
-          *reinterpret_cast<uint4*>(row + (G >> 1) * kChunkBytes + (((4 * (G & 1) + y) ^ (key & 7)) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
-        }
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  // Waits for a free stage, fills it (a step-key window by TMA) and arrives.
+  auto fill = [&](auto is_v, int i, const uint8_t* raw, uint32_t live) -> bool {
+    constexpr bool v = decltype(is_v)::value;
+    const int s = i & 1;
+    const uint32_t full = bar((v ? BAR_VFULL : BAR_KFULL) + s), tile = (v ? L::kOffV : kOffK) + (uint32_t)s * kTileBytes;
+    if (i >= 2 && !warp_wait_bar(bar((v ? BAR_VEMPTY : BAR_KEMPTY) + s), (uint32_t)((i / 2 - 1) & 1), abort_flag, a.err))
+      return false;
+    if (i < bp.npb) {
+      convert(is_v, raw, tile, i, live);
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
+    } else if (lane == 0) {
+      if (w == 0) {
+        const CUtensorMap* map = v ? &tm_vs : &tm_ks;
+        const int win = bp.wins[i - bp.npb];
+        mbar_expect_tx(full, kTileBytes);
+        tma_load_4d(sb + tile, map, 0, g, win * 128, b, full);
+        tma_load_4d(sb + tile + kChunkBytes, map, 64, g, win * 128, b, full);
+      } else {
+        mbar_arrive(full);
+      }
     }
+    return true;
+  };
+  static_assert(L::kRing == 2 && kRawTurns == 2, "stage and raw slot of a turn: its parity");
+  // entries of blocks j + 1 (e1), j + 2 (e2) and j + 3 (e3) at the start of turn
+  // j; which groups of blocks j - 1, j and j + 1 lie on a valid page
+  bool ok = !prm.starve;
+  int e1 = -1, e2 = -1, e3 = -1;
+  uint32_t lv = 0, lk = 0, ln = 0;
+  if (ok) {
+    const int e0 = load_entries(0);
+    e1 = load_entries(1);
+    e2 = load_entries(2);
+    copy_turn(0, e0, -1);
+    copy_turn(1, e1, e0);
+    lk = __ballot_sync(0xffffffffu, e0 >= 0);
+    ln = __ballot_sync(0xffffffffu, e1 >= 0);
+  }
+  for (int j = 0; ok && j <= bp.nb; ++j) {
+    e3 = load_entries(j + 3);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRawTurns - 1) : "memory");
+    __syncwarp();
+    const uint8_t* raw = smem + raw0 + (uint32_t)(j & 1) * kRawTurn;
+    if (j < bp.nb) ok = fill(std::false_type{}, j, raw, lk);
+    if (ok && j >= 1) ok = fill(std::true_type{}, j - 1, raw + kRawPer * kRawGroup, lv);
+    if (!ok) break;
     __syncwarp();                                          // every lane has read the raw slot: refill it
-    advance(p + kRawPhases);
+    copy_turn(j + 2, e2, e1);
+    lv = lk;
+    lk = ln;
+    ln = __ballot_sync(0xffffffffu, e2 >= 0);
+    e1 = e2;
+    e2 = e3;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (bad) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
   if (w == 0 && lane == 0 && *abort_flag) {
     // drain: no copy may still write shared memory when the CTA moves on
     wait_quiet(bar(BAR_Q), 0);
-    for (int i = max(0, bp.nb - kStages); i < bp.nb; ++i) {
-      if (i < bp.npb) continue;
-      wait_quiet(bar(BAR_KFULL + i % kStages), (uint32_t)((i / kStages) & 1));
-      wait_quiet(bar(BAR_VFULL + i % L::kVStages), (uint32_t)((i / L::kVStages) & 1));
+    for (int i = max(bp.npb, bp.nb - L::kRing); i < bp.nb; ++i) {
+      wait_quiet(bar(BAR_KFULL + i % L::kRing), (uint32_t)((i / L::kRing) & 1));
+      wait_quiet(bar(BAR_VFULL + i % L::kRing), (uint32_t)((i / L::kRing) & 1));
     }
   }
   __syncwarp();
@@ -325,16 +349,21 @@ __device__ __forceinline__ void append_kv4(const AttnArgs& a, const int32_t* tab
 }
 
 // ------------------------------------------------------------------ the kernel
-// 18 (KV4: 20) warps: an SMSP hosts up to five of them, so a thread may hold at
-// most 16384 / (5 * 32) -> 96 registers.
+// 18 warps: two SMSPs host five of them, so a thread may hold at most
+// 16384 / (5 * 32) -> 96 registers.  KV4: 24 warps, six an SMSP, launched with 80
+// registers a thread; the two warpgroups of the MMA issuer and the dequantising
+// warps give registers up to the four softmax warpgroups for the main loop:
+// 256 * 48 + 512 * 96 = 768 * 80.
+constexpr int kRegsKv4 = 80, kRegsOther = 48, kRegsSoft = 96;
+static_assert(256 * kRegsOther + 512 * kRegsSoft <= 768 * kRegsKv4, "register split");
+template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <bool KV4>
-__global__ void __maxnreg__(96)
-attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kp,
-                 const __grid_constant__ CUtensorMap tm_vp, const __grid_constant__ CUtensorMap tm_ks,
-                 const __grid_constant__ CUtensorMap tm_vs, const Tc05Params prm) {
+__device__ __forceinline__ void attn_body(const CUtensorMap& tm_q, const CUtensorMap& tm_kp, const CUtensorMap& tm_vp,
+                                          const CUtensorMap& tm_ks, const CUtensorMap& tm_vs, const Tc05Params& prm) {
   using L = Tc<KV4>;
-  constexpr uint32_t kOffBar = L::kOffBar, kOffMisc = L::kOffMisc, kOffRed = L::kOffRed, kOffOk = L::kOffOk;
-  constexpr int kThreads = L::kThreads, kVStages = L::kVStages, kSoft0 = L::kSoft0;
+  constexpr uint32_t kOffV = L::kOffV, kOffBar = L::kOffBar, kOffMisc = L::kOffMisc, kOffRed = L::kOffRed, kOffOk = L::kOffOk;
+  constexpr int kThreads = L::kThreads, kRing = L::kRing, kSoft0 = L::kSoft0;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
   const uint32_t sb = smem_u32(smem);
@@ -425,11 +454,77 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   float olse = -INFINITY;
   bool owrite = false;
 
+  // ------------------------------------------------------------------ MMA issuer
+  auto issue_mmas = [&]() {
+    // Block b belongs to softmax set t = b & 1, which owns S_t and O_t in TMEM.
+    // Order: S(0), S(1); then per block b: PV_t(b) and, behind it in the same
+    // in-order MMA pipe, S(b+2) into S_t (the columns PV_t(b) reads P from).
+    if (lane == 0) {
+      bool ok = wait_bar(bar(BAR_Q), 0, abort_flag, a.err);
+      fence_after();
+      // Operand descriptors: a descriptor's start-address field is the shared
+      // address / 16 (below 2^14 here), so a tile at base + delta has the
+      // descriptor of base plus delta / 16.  Q's eight are fixed; a stage's
+      // K and V ones are its ring slot's base plus constants, formed ahead of
+      // the eight-MMA asm blocks.
+      uint64_t dq[8];
+#pragma unroll
+      for (int kc = 0; kc < 8; ++kc) dq[kc] = desc_k_sw128(sb + kOffQ + (kc >> 2) * kChunkBytes + (kc & 3) * 32);
+      const uint64_t dk0 = desc_k_sw128(sb + kOffK), dv0 = desc_mn_sw128(sb + kOffV, kChunkBytes);
+      auto issue_s = [&](int blk) -> bool {
+        const int st = blk % kRing, t = blk & 1;
+        if (!wait_bar(bar(BAR_KFULL + st), (uint32_t)((blk / kRing) & 1), abort_flag, a.err)) return false;
+        TIDAR_TRACE_AT(256 + min(blk, 255));
+        fence_after();
+        const uint64_t kbase = dk0 + (uint64_t)((st * kTileBytes) >> 4);
+        uint64_t dk[8];
+#pragma unroll
+        for (int kc = 0; kc < 8; ++kc) dk[kc] = kbase + (uint64_t)(((kc >> 2) * kChunkBytes + (kc & 3) * 32) >> 4);
+        mma_ss_x8(tmem + col_s(t), dq, dk, kIdescS, 0u);
+        mma_commit(bar(BAR_SFULL + t));
+        mma_commit(bar(BAR_KEMPTY + st));
+        TIDAR_TRACE_AT(512 + min(blk, 255));
+        return true;
+      };
+      if (ok) ok = issue_s(0);
+      if (ok && bp.nb > 1) ok = issue_s(1);
+      for (int b2 = 0; ok && b2 < bp.nb; ++b2) {
+        const int st = b2 % kRing, t = b2 & 1, j = b2 >> 1;
+        if (!wait_bar(bar(BAR_VFULL + st), (uint32_t)((b2 / kRing) & 1), abort_flag, a.err)) break;
+        if (!wait_bar(bar(BAR_PFULL + t), (uint32_t)(j & 1), abort_flag, a.err)) break;
+        fence_after();
+        const uint64_t vbase = dv0 + (uint64_t)((st * kTileBytes) >> 4);
+        uint32_t pa[8];
+        uint64_t dv[8];
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          pa[kk] = tmem + col_s(t) + p_col(kk);
+          dv[kk] = vbase + (uint64_t)((kk * 2048) >> 4);
+        }
+        mma_ts_x8(tmem + col_o(t), pa, dv, kIdescPV, j > 0 ? 1u : 0u);
+        mma_commit(bar(BAR_PVDONE + t));
+        mma_commit(bar(BAR_VEMPTY + st));
+        TIDAR_TRACE_AT(768 + min(b2, 255));
+        if (b2 + 2 < bp.nb && !issue_s(b2 + 2)) break;
+      }
+      // every MMA issued above has completed before TMEM is released
+      mma_commit(bar(BAR_FINAL));
+      wait_quiet(bar(BAR_FINAL), 0);
+    }
+  };
+
   if (bp.nb == 0) {
     // This split holds no prefix keys of sequence b (only possible with
     // nsplit > 1): it contributes an empty partial (lse = -inf) to the merge.
-  } else if (KV4 && warp > L::kMma && warp < kSoft0) {
-    if constexpr (KV4) dequantise(prm, tm_q, tm_ks, tm_vs, smem, sb, bp, table, b, g, rho0, abort_flag);
+  } else if (KV4 && warp < kSoft0) {
+    // one instruction for whole warpgroups: registers down, the roles, up again
+    if constexpr (KV4) {
+      regs_dec<kRegsOther>();
+      if (warp == L::kMma) issue_mmas();
+      else dequantise(prm, tm_q, tm_ks, tm_vs, smem, sb, bp, table, b, g, rho0, abort_flag);
+      __syncwarp();
+      regs_inc<kRegsKv4>();
+    }
   } else if (!KV4 && warp == 0) {
     // ---------------------------------------------------------------- producer
     // Separate K and V rings (3 stages each): a K stage is refilled as soon as
@@ -547,65 +642,11 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         wait_quiet(bar(BAR_Q), 0);
       }
     }
-  } else if (warp == L::kMma) {
-    // ---------------------------------------------------------------- MMA issuer
-    // Block b belongs to softmax set t = b & 1, which owns S_t and O_t in TMEM.
-    // Order: S(0), S(1); then per block b: PV_t(b) and, behind it in the same
-    // in-order MMA pipe, S(b+2) into S_t (the columns PV_t(b) reads P from).
-    if (lane == 0) {
-      bool ok = wait_bar(bar(BAR_Q), 0, abort_flag, a.err);
-      fence_after();
-      // Operand descriptors: a descriptor's start-address field is the shared
-      // address / 16 (below 2^14 here), so a tile at base + delta has the
-      // descriptor of base plus delta / 16.  Q's eight are fixed; a stage's
-      // K and V ones are its ring slot's base plus constants, formed ahead of
-      // the eight-MMA asm blocks.
-      uint64_t dq[8];
-#pragma unroll
-      for (int kc = 0; kc < 8; ++kc) dq[kc] = desc_k_sw128(sb + kOffQ + (kc >> 2) * kChunkBytes + (kc & 3) * 32);
-      const uint64_t dk0 = desc_k_sw128(sb + kOffK), dv0 = desc_mn_sw128(sb + kOffV, kChunkBytes);
-      auto issue_s = [&](int blk) -> bool {
-        const int st = blk % kStages, t = blk & 1;
-        if (!wait_bar(bar(BAR_KFULL + st), (uint32_t)((blk / kStages) & 1), abort_flag, a.err)) return false;
-        TIDAR_TRACE_AT(256 + min(blk, 255));
-        fence_after();
-        const uint64_t kbase = dk0 + (uint64_t)((st * kTileBytes) >> 4);
-        uint64_t dk[8];
-#pragma unroll
-        for (int kc = 0; kc < 8; ++kc) dk[kc] = kbase + (uint64_t)(((kc >> 2) * kChunkBytes + (kc & 3) * 32) >> 4);
-        mma_ss_x8(tmem + col_s(t), dq, dk, kIdescS, 0u);
-        mma_commit(bar(BAR_SFULL + t));
-        mma_commit(bar(BAR_KEMPTY + st));
-        TIDAR_TRACE_AT(512 + min(blk, 255));
-        return true;
-      };
-      if (ok) ok = issue_s(0);
-      if (ok && bp.nb > 1) ok = issue_s(1);
-      for (int b2 = 0; ok && b2 < bp.nb; ++b2) {
-        const int st = b2 % kVStages, t = b2 & 1, j = b2 >> 1;
-        if (!wait_bar(bar(BAR_VFULL + st), (uint32_t)((b2 / kVStages) & 1), abort_flag, a.err)) break;
-        if (!wait_bar(bar(BAR_PFULL + t), (uint32_t)(j & 1), abort_flag, a.err)) break;
-        fence_after();
-        const uint64_t vbase = dv0 + (uint64_t)((st * kTileBytes) >> 4);
-        uint32_t pa[8];
-        uint64_t dv[8];
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          pa[kk] = tmem + col_s(t) + p_col(kk);
-          dv[kk] = vbase + (uint64_t)((kk * 2048) >> 4);
-        }
-        mma_ts_x8(tmem + col_o(t), pa, dv, kIdescPV, j > 0 ? 1u : 0u);
-        mma_commit(bar(BAR_PVDONE + t));
-        mma_commit(bar(BAR_VEMPTY + st));
-        TIDAR_TRACE_AT(768 + min(b2, 255));
-        if (b2 + 2 < bp.nb && !issue_s(b2 + 2)) break;
-      }
-      // every MMA issued above has completed before TMEM is released
-      mma_commit(bar(BAR_FINAL));
-      wait_quiet(bar(BAR_FINAL), 0);
-    }
+  } else if (!KV4 && warp == L::kMma) {
+    issue_mmas();
   } else {
     // ---------------------------------------------------------------- softmax
+    if constexpr (KV4) regs_inc<kRegsSoft>();
     // Sixteen warps from kSoft0.  Set t (block parity) = (warp-kSoft0)/8 owns S_t and
     // O_t; within a set, half hf = ((warp-kSoft0)/4)&1 takes columns [64hf, 64hf+64) of the rows of
     // TMEM lane quarter warp%4.  One thread = one half row.  The two halves of a
@@ -657,7 +698,7 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if (live && ok) {
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         uint32_t x[64];
-        tmem_ld64(trow + scol, x);
+        ld_half_row<KV4>(trow + scol, x);
         tmem_wait_ld();
         if (!full) {
           // masked block (rare): invisible keys become -inf in TMEM too, so
@@ -703,7 +744,7 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint64_t sl2x2 = f2_make(sl2, sl2), nbx2 = f2_make(nbase, nbase);
         uint64_t ls2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
         uint32_t x[64];
-        tmem_ld64(trow + scol, x);
+        ld_half_row<KV4>(trow + scol, x);
         tmem_wait_ld();
         uint32_t pk[32];
         // The same loop for full and masked blocks (invisible keys hold -inf
@@ -811,6 +852,10 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     owrite = write;
     olse = lse;
+    if constexpr (KV4) {
+      __syncwarp();
+      regs_dec<kRegsKv4>();
+    }
     if (warp == 4 && lane == 0) TIDAR_TRACE_AT(1538);
   }
 
@@ -914,6 +959,22 @@ attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   }
 }
 
+__global__ void __maxnreg__(96)
+attn_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kp,
+                 const __grid_constant__ CUtensorMap tm_vp, const __grid_constant__ CUtensorMap tm_ks,
+                 const __grid_constant__ CUtensorMap tm_vs, const __grid_constant__ Tc05Params prm) {
+  attn_body<false>(tm_q, tm_kp, tm_vp, tm_ks, tm_vs, prm);
+}
+__global__ void __launch_bounds__(Tc<true>::kThreads, 1)
+attn_kv4_tc05_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ks,
+                     const __grid_constant__ CUtensorMap tm_vs, const __grid_constant__ Tc05Params prm) {
+  attn_body<true>(tm_q, tm_ks, tm_vs, tm_ks, tm_vs, prm);
+}
+template <bool KV4> constexpr auto kernel_of() {
+  if constexpr (KV4) return attn_kv4_tc05_kernel;
+  else return attn_tc05_kernel;
+}
+
 // ------------------------------------------------------------------ host side
 // The kernel's dynamic shared memory opt-in, once per device.
 template <bool KV4>
@@ -924,7 +985,7 @@ cudaError_t set_smem_attr() {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorNotSupported;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(attn_tc05_kernel<KV4>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<KV4>::kSmem);
+    e = cudaFuncSetAttribute(kernel_of<KV4>(), cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<KV4>::kSmem);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
@@ -962,7 +1023,6 @@ cudaError_t launch_t(const AttnArgs& a, cudaStream_t s) {
     if (!encode(&tks, a.k_blk, 4, dims, str, box)) return cudaErrorNotSupported;
     if (!encode(&tvs, a.v_blk, 4, dims, str, box)) return cudaErrorNotSupported;
   }
-  if constexpr (KV4) tkp = tks, tvp = tvs;              // the kernel reads the pages itself
   cudaError_t e = set_smem_attr<KV4>();
   if (e != cudaSuccess) return e;
   const bool clu = a.nsplit > 1 && a.cluster_merge;
@@ -971,8 +1031,11 @@ cudaError_t launch_t(const AttnArgs& a, cudaStream_t s) {
   const dim3 grid(prm.tiles, a.nsplit, a.B * a.Hkv);
   // with the cluster merge, the splits of one (b, g, tile) form a cluster
   const dim3 cluster(1, clu ? a.nsplit : 1, 1);
-  return launch_clustered(attn_tc05_kernel<KV4>, grid, cluster, Tc<KV4>::kThreads, Tc<KV4>::kSmem, s, tq, tkp, tvp, tks,
-                          tvs, prm);
+  if constexpr (KV4)                                   // the kernel reads the pages itself
+    return launch_clustered(attn_kv4_tc05_kernel, grid, cluster, Tc<KV4>::kThreads, Tc<KV4>::kSmem, s, tq, tks, tvs, prm);
+  else
+    return launch_clustered(attn_tc05_kernel, grid, cluster, Tc<KV4>::kThreads, Tc<KV4>::kSmem, s, tq, tkp, tvp, tks, tvs,
+                            prm);
 }
 
 template <bool KV4>
@@ -984,7 +1047,7 @@ int resident_clusters_t(int ns) {
   if (cache[dev][ns]) return cache[dev][ns] - 1;
   int n = 0;
   if (set_smem_attr<KV4>() == cudaSuccess &&
-      (ns <= 8 || cudaFuncSetAttribute(attn_tc05_kernel<KV4>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+      (ns <= 8 || cudaFuncSetAttribute(kernel_of<KV4>(), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
                       cudaSuccess)) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, ns, 1);
@@ -997,7 +1060,7 @@ int resident_clusters_t(int ns) {
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, attn_tc05_kernel<KV4>, &cfg) != cudaSuccess) n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel_of<KV4>(), &cfg) != cudaSuccess) n = 0;
   }
   cudaGetLastError();
   cache[dev][ns] = n + 1;
