@@ -187,56 +187,65 @@ __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensor
   const int kk = ((lane >> 3) & 3) + 4 * ((lane >> 2) & 1), y = lane & 3;
   const uint32_t stride32 = (uint32_t)page_stride;       // below 2^32: 65535 heads at most
   const uint32_t raw0 = L::kOffRaw + (uint32_t)w * (kRawTurns * kRawTurn);
-  const uint32_t own = (uint32_t)(kk * 64 + y * 16), scale_off = (uint32_t)ps * 64u + 16u * lane;
+  const uint32_t own = (uint32_t)(kk * 64 + y * 16);
   bool bad = false;
-  // Table entry of group `lane` (16 of them) of prefix block i: -1 where there
-  // is no key or no valid page.
+  // Table entry of group `lane` (16 of them) of prefix block i, -1 where there is
+  // no key; checked a turn later, when it has arrived.
   auto load_entries = [&](int i) -> int {
     const int key = bp.k0 + 128 * i + 8 * (lane & 15);
-    if (i >= bp.npb || key >= bp.kend) return -1;
-    const int pg = table[key >> lps];
-    if (page_ok(pg, a.num_pages)) return pg;
-    bad = true;
-    return -1;
+    return i < bp.npb && key < bp.kend ? table[key >> lps] : -1;
   };
-  // This warp's groups of block i: (w + i) % 7, + 7, + 14 (below 16).
-  auto first_group = [&](int i) -> int { return (w + i) % kDqWarps; };
-  auto copy_block = [&](const uint8_t* base, uint32_t dst, int i, int entries) {
-    const int q0 = first_group(i);
+  // Turn j converts K(j) and V(j - 1); this warp's groups of block i are q, q + 7,
+  // q + 14 (below 16), q = (w + i) % 7.  The copies of a turn (one commit group) go
+  // into raw slot j % 2: the codes a group an instruction, the scales of all six
+  // groups in one (lanes 4t .. 4t+3 those of group t).  e_k, e_v: the checked
+  // table entries of blocks j and j - 1; q_k, q_v their first groups.
+  const int st_grp = lane >> 2;                            // 0..2 K, 3..5 V, above: none
+  const bool st_v = st_grp >= 3;
+  const uint32_t st_dst = sb + raw0 + (uint32_t)st_grp * kRawGroup + 512u + 16u * (lane & 3);
+  const uint8_t* st_base = (st_v ? vbase : kbase) + (size_t)ps * 64 + 16 * (lane & 3);
+  const int st_q = kDqWarps * (st_v ? st_grp - 3 : st_grp);
+  auto copy_turn = [&](int j, int e_k, int e_v, int q_k, int q_v) {
+    const uint32_t slot = (uint32_t)(j & 1) * kRawTurn;
 #pragma unroll
-    for (int j = 0; j < kRawPer; ++j) {
-      const int q = q0 + kDqWarps * j;
-      const int pg = __shfl_sync(0xffffffffu, entries, q & 15);
+    for (int t = 0; t < 2 * kRawPer; ++t) {
+      const bool v = t >= kRawPer;
+      const int q = (v ? q_v : q_k) + kDqWarps * (v ? t - kRawPer : t);
+      const int pg = __shfl_sync(0xffffffffu, v ? e_v : e_k, q & 15);
       if (q < 16 && pg >= 0) {
-        const uint32_t row = (uint32_t)(bp.k0 + 128 * i + 8 * q) & (uint32_t)(ps - 1);
-        const uint8_t* src = base + (uint64_t)(uint32_t)pg * stride32;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * kRawGroup), "l"(src + (row * 64 + own))
+        const uint32_t row = (uint32_t)(bp.k0 + 128 * (v ? j - 1 : j) + 8 * q) & (uint32_t)(ps - 1);
+        const uint8_t* src = (v ? vbase : kbase) + (uint64_t)(uint32_t)pg * stride32 + (row * 64 + own);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sb + raw0 + slot + t * kRawGroup + 16u * lane), "l"(src)
                      : "memory");
-        if (lane < 4)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * kRawGroup + 512u),
-                       "l"(src + (scale_off + row * 8))
-                       : "memory");
       }
     }
-  };
-  // Turn j converts K(j) and V(j - 1).  Its copies (one commit group) go into
-  // raw slot j % 2; e_k, e_v are the table entries of blocks j and j - 1.
-  auto copy_turn = [&](int j, int e_k, int e_v) {
-    const uint32_t dst = sb + raw0 + (uint32_t)(j & 1) * kRawTurn + 16u * lane;
-    if (j < bp.npb) copy_block(kbase, dst, j, e_k);
-    if (j >= 1 && j <= bp.npb) copy_block(vbase, dst + kRawPer * kRawGroup, j - 1, e_v);
+    const int q = (st_v ? q_v : q_k) + st_q;
+    const int pk = __shfl_sync(0xffffffffu, e_k, q & 15), pv = __shfl_sync(0xffffffffu, e_v, q & 15);
+    const int pg = st_v ? pv : pk;
+    if (lane < 8 * kRawPer && q < 16 && pg >= 0) {
+      const uint32_t row = (uint32_t)(bp.k0 + 128 * (st_v ? j - 1 : j) + 8 * q) & (uint32_t)(ps - 1);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(st_dst + slot),
+                   "l"(st_base + (uint64_t)(uint32_t)pg * stride32 + row * 8)
+                   : "memory");
+    }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  auto checked = [&](int e, int i) -> int {                // a page that does not exist: reported, not copied
+    if (e >= 0 && e < a.num_pages) return e;
+    if (i < bp.npb && bp.k0 + 128 * i + 8 * (lane & 15) < bp.kend) bad = true;
+    return -1;
+  };
   // Converts this warp's groups of block i from `raw` into the ring tile.
-  auto convert = [&](auto is_v, const uint8_t* raw, uint32_t tile, int i, uint32_t live) {
-    const int q0 = first_group(i), left = bp.kend - bp.k0 - 128 * i;      // keys of the block that exist
+  auto convert = [&](auto is_v, const uint8_t* raw, uint32_t tile, int i, int q0, uint32_t live) {
+    const int left = bp.kend - bp.k0 - 128 * i;             // keys of the block that exist
+    const bool whole = left >= 128 && (live & 0xffffu) == 0xffffu;
 #pragma unroll
     for (int j = 0; j < kRawPer; ++j) {
       const int q = q0 + kDqWarps * j, key = 8 * q + kk;
       if (q >= 16) break;
       uint4 c = *reinterpret_cast<const uint4*>(raw + j * kRawGroup + 16 * lane);
       uint2 sc = *reinterpret_cast<const uint2*>(raw + j * kRawGroup + 512 + 8 * kk);
-      if (key >= left || !((live >> q) & 1u)) c = make_uint4(0, 0, 0, 0), sc = make_uint2(0, 0);
+      if (!whole && (key >= left || !((live >> q) & 1u))) c = make_uint4(0, 0, 0, 0), sc = make_uint2(0, 0);
       uint32_t words[4] = {c.x, c.y, c.z, c.w};
       if constexpr (decltype(is_v)::value) {
         const uint32_t raw4[4] = {c.x, c.y, c.z, c.w};
@@ -260,14 +269,14 @@ __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensor
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   };
   // Waits for a free stage, fills it (a step-key window by TMA) and arrives.
-  auto fill = [&](auto is_v, int i, const uint8_t* raw, uint32_t live) -> bool {
+  auto fill = [&](auto is_v, int i, const uint8_t* raw, int q0, uint32_t live) -> bool {
     constexpr bool v = decltype(is_v)::value;
     const int s = i & 1;
     const uint32_t full = bar((v ? BAR_VFULL : BAR_KFULL) + s), tile = (v ? L::kOffV : kOffK) + (uint32_t)s * kTileBytes;
     if (i >= 2 && !warp_wait_bar(bar((v ? BAR_VEMPTY : BAR_KEMPTY) + s), (uint32_t)((i / 2 - 1) & 1), abort_flag, a.err))
       return false;
     if (i < bp.npb) {
-      convert(is_v, raw, tile, i, live);
+      convert(is_v, raw, tile, i, q0, live);
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
     } else if (lane == 0) {
@@ -284,35 +293,39 @@ __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensor
     return true;
   };
   static_assert(L::kRing == 2 && kRawTurns == 2, "stage and raw slot of a turn: its parity");
-  // entries of blocks j + 1 (e1), j + 2 (e2) and j + 3 (e3) at the start of turn
-  // j; which groups of blocks j - 1, j and j + 1 lie on a valid page
+  // At the start of turn j: the checked entries of blocks j + 1 (e1) and j + 2
+  // (e2); which groups of blocks j - 1, j, j + 1 lie on a valid page (lv, lk, ln);
+  // the first group of block j (qk).
   bool ok = !prm.starve;
-  int e1 = -1, e2 = -1, e3 = -1;
+  int e1 = -1, e2 = -1, qk = w;
   uint32_t lv = 0, lk = 0, ln = 0;
+  auto step = [](int q, int by) -> int { q += by; return q >= kDqWarps ? q - kDqWarps : q; };
   if (ok) {
-    const int e0 = load_entries(0);
-    e1 = load_entries(1);
-    e2 = load_entries(2);
-    copy_turn(0, e0, -1);
-    copy_turn(1, e1, e0);
+    const int r0 = load_entries(0), r1 = load_entries(1), r2 = load_entries(2);
+    const int e0 = checked(r0, 0);
+    e1 = checked(r1, 1);
+    e2 = checked(r2, 2);
+    copy_turn(0, e0, -1, qk, 0);
+    copy_turn(1, e1, e0, step(qk, 1), qk);
     lk = __ballot_sync(0xffffffffu, e0 >= 0);
     ln = __ballot_sync(0xffffffffu, e1 >= 0);
   }
   for (int j = 0; ok && j <= bp.nb; ++j) {
-    e3 = load_entries(j + 3);
+    const int e3 = load_entries(j + 3);
     asm volatile("cp.async.wait_group %0;" ::"n"(kRawTurns - 1) : "memory");
     __syncwarp();
     const uint8_t* raw = smem + raw0 + (uint32_t)(j & 1) * kRawTurn;
-    if (j < bp.nb) ok = fill(std::false_type{}, j, raw, lk);
-    if (ok && j >= 1) ok = fill(std::true_type{}, j - 1, raw + kRawPer * kRawGroup, lv);
+    if (j < bp.nb) ok = fill(std::false_type{}, j, raw, qk, lk);
+    if (ok && j >= 1) ok = fill(std::true_type{}, j - 1, raw + kRawPer * kRawGroup, step(qk, kDqWarps - 1), lv);
     if (!ok) break;
     __syncwarp();                                          // every lane has read the raw slot: refill it
-    copy_turn(j + 2, e2, e1);
+    copy_turn(j + 2, e2, e1, step(qk, 2), step(qk, 1));
     lv = lk;
     lk = ln;
     ln = __ballot_sync(0xffffffffu, e2 >= 0);
     e1 = e2;
-    e2 = e3;
+    e2 = checked(e3, j + 3);
+    qk = step(qk, 1);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (bad) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
