@@ -159,6 +159,14 @@ __device__ __forceinline__ void ld_half_row(uint32_t taddr, uint32_t (&x)[64]) {
 }
 
 // ------------------------------------------------------------------ 4-bit cache
+// A 16-byte asynchronous copy, predicated (a branch around each costs more than
+// the copy).
+__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst),
+      "l"(src), "r"((int)on)
+      : "memory");
+}
 // The dequantising warps (1 .. kDqWarps) of a KV4 CTA: Q, then the blocks of
 // the K and V rings.  A group is 8 neighbouring keys of one operand; lane
 // (kk, y), kk = (lane/8) + 4 (lane/4 % 2), y = lane % 4, copies and converts
@@ -212,22 +220,16 @@ __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensor
       const bool v = t >= kRawPer;
       const int q = (v ? q_v : q_k) + kDqWarps * (v ? t - kRawPer : t);
       const int pg = __shfl_sync(0xffffffffu, v ? e_v : e_k, q & 15);
-      if (q < 16 && pg >= 0) {
-        const uint32_t row = (uint32_t)(bp.k0 + 128 * (v ? j - 1 : j) + 8 * q) & (uint32_t)(ps - 1);
-        const uint8_t* src = (v ? vbase : kbase) + (uint64_t)(uint32_t)pg * stride32 + (row * 64 + own);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sb + raw0 + slot + t * kRawGroup + 16u * lane), "l"(src)
-                     : "memory");
-      }
+      const uint32_t row = (uint32_t)(bp.k0 + 128 * (v ? j - 1 : j) + 8 * q) & (uint32_t)(ps - 1);
+      const uint8_t* src = (v ? vbase : kbase) + (uint64_t)(uint32_t)pg * stride32 + (row * 64 + own);
+      cp_async16_if(sb + raw0 + slot + t * kRawGroup + 16u * lane, src, q < 16 && pg >= 0);
     }
     const int q = (st_v ? q_v : q_k) + st_q;
     const int pk = __shfl_sync(0xffffffffu, e_k, q & 15), pv = __shfl_sync(0xffffffffu, e_v, q & 15);
     const int pg = st_v ? pv : pk;
-    if (lane < 8 * kRawPer && q < 16 && pg >= 0) {
-      const uint32_t row = (uint32_t)(bp.k0 + 128 * (st_v ? j - 1 : j) + 8 * q) & (uint32_t)(ps - 1);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(st_dst + slot),
-                   "l"(st_base + (uint64_t)(uint32_t)pg * stride32 + row * 8)
-                   : "memory");
-    }
+    const uint32_t row = (uint32_t)(bp.k0 + 128 * (st_v ? j - 1 : j) + 8 * q) & (uint32_t)(ps - 1);
+    cp_async16_if(st_dst + slot, st_base + (uint64_t)(uint32_t)pg * stride32 + row * 8,
+                  lane < 8 * kRawPer && q < 16 && pg >= 0);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto checked = [&](int e, int i) -> int {                // a page that does not exist: reported, not copied
