@@ -205,5 +205,9 @@ LinearPlan plan_linear(int T, int K, int N);
 // of the reduction are partly outside the tensors, where TMA reads zeros.
 LinearPlan plan_linear_any(int T, int K, int N);
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
+// Mode 2 for many rows, on pairs of SMs (no workspace); wanted: the shapes for
+// which it is the faster kernel.
+bool linear_pair_wanted(int T, int K, int N);
+cudaError_t launch_linear_pair(const LinearArgs& a, cudaStream_t s);
 
 }  // namespace tidar

@@ -51,6 +51,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "linear_act.cuh"
 #include "sm100.cuh"
 
 namespace tidar {
@@ -161,21 +162,6 @@ __device__ __forceinline__ long long zone_position(int k, int row, int P) {
 __device__ __forceinline__ int lin_group(const LinParams& prm, int tt, int ft) { return tt * prm.ftiles + ft; }
 __device__ __forceinline__ size_t lin_part_offset(const LinParams& prm, int tt, int ft, int split) {
   return ((size_t)lin_group(prm, tt, ft) * prm.ksplit + split) * (size_t)prm.nt * 128;
-}
-
-// The activations of the fused epilogue, on the fp32 sum.
-__device__ __forceinline__ float lin_act(float v, int act) {
-  switch (act) {
-    case TIDAR_ACT_RELU: return v < 0.f ? 0.f : v;        // NaN stays NaN
-    case TIDAR_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    // 0.5 v (1 + tanh u) = v sigmoid(2u): no cancellation in the negative tail
-    case TIDAR_ACT_GELU_TANH: {
-      const float u2 = 1.5957691216057308f * fmaf(0.044715f * v * v, v, v);
-      return v / (1.f + __expf(-u2));
-    }
-    case TIDAR_ACT_SILU: return v / (1.f + __expf(-v));
-  }
-  return v;
 }
 
 // Sum of the KS splits' partials of tokens [tlo, thi) of the tile and the
