@@ -30,6 +30,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import re
 
@@ -716,31 +717,37 @@ def reserve(cache, pool, k, *, max_prefix_len, returned=None, num_returned=None,
     _check(st, "tidar_reserve")
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream     # handle of a device's current stream
+_current_device = torch._C._cuda_getDevice
+
+
 @contextlib.contextmanager
-def _launching(dev, stream):
-    """The handle of the stream a call on `dev` is queued on (`stream`, or the
-    current one of that device), with the device current.  What the call
-    allocates belongs to that stream, so it is not handed out again before the
-    call is done."""
-    if not isinstance(dev, torch.device) or dev.type != "cuda":
+def _on(dev, stream):
+    """`dev` and `stream` (None: that device's current one) made current.  What
+    a call allocates inside belongs to that stream, so it is not handed out again
+    before the call is done."""
+    if dev.type != "cuda":
         raise ValueError(f"the call's tensors are on {dev}, not on a CUDA device")
-    if stream is None:
-        if dev.index == torch.cuda.current_device():
-            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-        else:
-            with torch.cuda.device(dev):
-                yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    else:
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the call's tensors are on {dev}")
-        with torch.cuda.device(dev), torch.cuda.stream(stream):
-            yield ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the call's tensors are on {dev}")
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        yield
+
+
+def _away(t, name, stream) -> bool:
+    """Whether a call on t has to be made under ``_on`` (the common call, on the
+    current device and its current stream, does without)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return stream is not None or t.device.index != _current_device()
 
 
 def _shaped(t, name, shape, dtype, dev):
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == dev and t.shape == shape and
+            t.is_contiguous()):
+        return
     _dev(t, name, dtype, dev)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} is {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} is {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def build_tables(page_table, ctx_lens, new_lens, pool, *, page_size, num_pages, max_rows, out=None,
@@ -751,6 +758,10 @@ def build_tables(page_table, ctx_lens, new_lens, pool, *, page_size, num_pages, 
     ``row_starts`` [B+1], ``slots`` [max_rows] int64 and ``positions`` [max_rows].
     ``out`` may bring any of them (``page_table`` and ``pool["free_count"]``
     themselves for an update in place); the inputs are otherwise left alone."""
+    if _away(page_table, "page_table", stream):
+        with _on(page_table.device, stream):
+            return build_tables(page_table, ctx_lens, new_lens, pool, page_size=page_size, num_pages=num_pages,
+                                max_rows=max_rows, out=out)
     _dev(page_table, "page_table", torch.int32)
     dev = page_table.device
     if page_table.dim() != 2:
@@ -764,23 +775,29 @@ def build_tables(page_table, ctx_lens, new_lens, pool, *, page_size, num_pages, 
     max_rows = int(max_rows)
     if max_rows < 0:
         raise ValueError(f"max_rows is {max_rows}")
-    res = dict(out) if out else {}
-    with _launching(dev, stream) as s:
-        for name, shape, dtype in (("page_table", (B, width), torch.int32), ("free_count", (1,), torch.int32),
-                                   ("row_starts", (B + 1,), torch.int32), ("slots", (max_rows,), torch.int64),
-                                   ("positions", (max_rows,), torch.int32)):
-            if name in res:
-                _shaped(res[name], name, shape, dtype, dev)
-            else:
-                res[name] = torch.empty(shape, dtype=dtype, device=dev)
-        d = TablesDesc(batch=B, page_size=int(page_size), num_pages=int(num_pages), max_pages_per_seq=width,
-                       max_rows=max_rows)
-        p = PagePool(free_pages=fp.data_ptr() or None, free_count=fc.data_ptr(), capacity=fp.numel())
-        st = lib().tidar_build_tables(ctypes.byref(d), _ptr(page_table), _ptr(ctx_lens), _ptr(new_lens),
-                                      ctypes.byref(p), _ptr(res["page_table"]), _ptr(res["free_count"]),
-                                      _ptr(res["row_starts"]), _ptr(res["slots"]), _ptr(res["positions"]), s)
-    _check(st, "tidar_build_tables")
-    return res
+    if out is None:
+        out = {}
+    new = page_table.new_empty
+    tab, cnt, sta, slo, pos = (out.get(n) for n in ("page_table", "free_count", "row_starts", "slots", "positions"))
+    tab = new((B, width)) if tab is None else tab
+    cnt = new((1,)) if cnt is None else cnt
+    sta = new((B + 1,)) if sta is None else sta
+    slo = new((max_rows,), dtype=torch.int64) if slo is None else slo
+    pos = new((max_rows,)) if pos is None else pos
+    if out:
+        _shaped(tab, "page_table", (B, width), torch.int32, dev)
+        _shaped(cnt, "free_count", (1,), torch.int32, dev)
+        _shaped(sta, "row_starts", (B + 1,), torch.int32, dev)
+        _shaped(slo, "slots", (max_rows,), torch.int64, dev)
+        _shaped(pos, "positions", (max_rows,), torch.int32, dev)
+    d = TablesDesc(B, int(page_size), int(num_pages), width, max_rows)
+    p = PagePool(fp.data_ptr() or None, fc.data_ptr(), fp.numel())
+    st = lib().tidar_build_tables(ctypes.byref(d), page_table.data_ptr(), ctx_lens.data_ptr(), new_lens.data_ptr(),
+                                  ctypes.byref(p), tab.data_ptr(), cnt.data_ptr(), sta.data_ptr(), slo.data_ptr(),
+                                  pos.data_ptr(), _raw_stream(dev.index))
+    if st:
+        _check(st, "tidar_build_tables")
+    return dict(page_table=tab, free_count=cnt, row_starts=sta, slots=slo, positions=pos)
 
 
 def kv4_page_bytes(page_size: int, head_dim: int) -> int:
@@ -799,6 +816,9 @@ def kv4_cache(num_pages, num_kv_heads, page_size, head_dim, page_table, seq_lens
                 page_table=page_table, seq_lens=seq_lens)
 
 
+_KV4_PAGE_SIZE = {ps * (D // 2 + D // 16) + (D << 32): ps for ps in (16, 32, 64, 128) for D in (64, 128)}
+
+
 def _kv4_page_size(cache, head_dim, dev):
     """page_size of a 4-bit cache whose rows are head_dim long."""
     kp, vp = cache["k_pages"], cache["v_pages"]
@@ -807,11 +827,11 @@ def _kv4_page_size(cache, head_dim, dev):
     if kp.dim() != 3 or vp.shape != kp.shape:
         raise ValueError(f"k_pages {tuple(kp.shape)} and v_pages {tuple(vp.shape)} must both be "
                          "[num_pages][Hkv][page_bytes]")
-    row = head_dim // 2 + head_dim // 16
-    if head_dim not in (64, 128) or kp.shape[2] % row or kp.shape[2] // row not in (16, 32, 64, 128):
+    ps = _KV4_PAGE_SIZE.get(kp.shape[2] + (head_dim << 32))
+    if ps is None:
         raise ValueError(f"pages of {kp.shape[2]} bytes do not hold 16, 32, 64 or 128 rows of {head_dim} dims "
                          "(64 or 128) in 4 bits")
-    return kp.shape[2] // row
+    return ps
 
 
 def _row_stride(t, name, dtype, dev):
@@ -834,55 +854,60 @@ def _kv4_desc(cache, k, v, slots):
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("rows must be CUDA tensors [rows][Hkv][D]")
     dev = k.device
-    d = Kv4Desc(rows=k.shape[0], num_kv_heads=k.shape[1], head_dim=k.shape[2], dtype=_dtype_code(k),
-                k_row_stride=_row_stride(k, "k_rows", k.dtype, dev),
-                v_row_stride=_row_stride(v, "v_rows", k.dtype, dev))
+    T, H, D = k.shape
+    ks, vs = _row_stride(k, "k_rows", k.dtype, dev), _row_stride(v, "v_rows", k.dtype, dev)
     if v.shape != k.shape:
         raise ValueError(f"k_rows {tuple(k.shape)} and v_rows {tuple(v.shape)} disagree")
-    d.page_size = _kv4_page_size(cache, k.shape[2], dev)
-    d.num_pages = cache["k_pages"].shape[0]
-    if cache["k_pages"].shape[1] != k.shape[1]:
-        raise ValueError(f"the cache holds {cache['k_pages'].shape[1]} heads, the rows {k.shape[1]}")
-    _shaped(slots, "slots", (k.shape[0],), torch.int64, dev)
-    return d, dev
+    ps = _kv4_page_size(cache, D, dev)
+    pages, heads = cache["k_pages"].shape[:2]
+    if heads != H:
+        raise ValueError(f"the cache holds {heads} heads, the rows {H}")
+    _shaped(slots, "slots", (T,), torch.int64, dev)
+    return Kv4Desc(T, H, D, ps, pages, _dtype_code(k), ks, vs)
 
 
 def kv4_append(cache, k_rows, v_rows, slots, *, stream=None):
     """Quantise rows [T][Hkv][D] (row strides allowed: a slice of a projection's
     output) and store them at ``slots`` [T] int64; a negative slot skips its row."""
-    d, dev = _kv4_desc(cache, k_rows, v_rows, slots)
-    with _launching(dev, stream) as s:
-        st = lib().tidar_kv4_append(ctypes.byref(d), _ptr(cache["k_pages"]), _ptr(cache["v_pages"]), _ptr(k_rows),
-                                    _ptr(v_rows), _ptr(slots), s)
-    _check(st, "tidar_kv4_append")
+    if _away(k_rows, "k_rows", stream):
+        with _on(k_rows.device, stream):
+            return kv4_append(cache, k_rows, v_rows, slots)
+    d = _kv4_desc(cache, k_rows, v_rows, slots)
+    st = lib().tidar_kv4_append(ctypes.byref(d), cache["k_pages"].data_ptr(), cache["v_pages"].data_ptr(),
+                                k_rows.data_ptr(), v_rows.data_ptr(), slots.data_ptr(),
+                                _raw_stream(k_rows.device.index))
+    if st:
+        _check(st, "tidar_kv4_append")
 
 
 def kv4_gather(cache, slots, *, head_dim=None, dtype=torch.bfloat16, out=None, stream=None):
     """The values stored at ``slots`` [T]: (k_rows, v_rows) [T][Hkv][D].  Rows
     whose slot is negative are left as they were (zeros when allocated here)."""
-    _dev(slots, "slots", torch.int64)
-    dev = slots.device
-    with _launching(dev, stream) as s:
-        if out is None:
-            if head_dim is None:
-                raise ValueError("head_dim is needed when out is not given")
-            if dtype not in (torch.float32, torch.bfloat16):
-                raise ValueError(f"unsupported dtype {dtype}")
-            shape = (slots.numel(), cache["k_pages"].shape[1], head_dim)
-            out = (torch.zeros(shape, dtype=dtype, device=dev), torch.zeros(shape, dtype=dtype, device=dev))
-        k, v = out
-        d, dev2 = _kv4_desc(cache, k, v, slots)
-        st = lib().tidar_kv4_gather(ctypes.byref(d), _ptr(cache["k_pages"]), _ptr(cache["v_pages"]), _ptr(slots),
-                                    _ptr(k), _ptr(v), s)
-    _check(st, "tidar_kv4_gather")
+    if _away(slots, "slots", stream):
+        with _on(slots.device, stream):
+            return kv4_gather(cache, slots, head_dim=head_dim, dtype=dtype, out=out)
+    if out is None:
+        if head_dim is None:
+            raise ValueError("head_dim is needed when out is not given")
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"unsupported dtype {dtype}")
+        both = torch.zeros((2, slots.numel(), cache["k_pages"].shape[1], head_dim), dtype=dtype, device=slots.device)
+        out = (both[0], both[1])
+    k, v = out
+    d = _kv4_desc(cache, k, v, slots)
+    if k.device != slots.device:
+        raise ValueError(f"out is on {k.device}, the call's tensors are on {slots.device}")
+    st = lib().tidar_kv4_gather(ctypes.byref(d), cache["k_pages"].data_ptr(), cache["v_pages"].data_ptr(),
+                                slots.data_ptr(), k.data_ptr(), v.data_ptr(), _raw_stream(slots.device.index))
+    if st:
+        _check(st, "tidar_kv4_gather")
     return k, v
 
 
 def step_attn_kv4_desc(q, k_blk, cache, k, max_prefix_len, scale=0.0, path="auto") -> StepDesc:
     B, R, Hq, D = q.shape
-    return StepDesc(batch=B, num_q_heads=Hq, num_kv_heads=k_blk.shape[2], head_dim=D, k=k,
-                    page_size=_kv4_page_size(cache, D, q.device), max_prefix_len=int(max_prefix_len),
-                    dtype=_dtype_code(q), softmax_scale=float(scale), path=_PATHS[path])
+    return StepDesc(B, Hq, k_blk.shape[2], D, k, _kv4_page_size(cache, D, q.device), int(max_prefix_len),
+                    _dtype_code(q), float(scale), _PATHS[path])
 
 
 def kv4_plan(desc: StepDesc) -> tuple[int, int, int]:
@@ -897,40 +922,64 @@ def step_attn_kv4_workspace_bytes(desc: StepDesc) -> int:
     return int(lib().tidar_step_attn_kv4_workspace_bytes(ctypes.byref(desc)))
 
 
+@functools.lru_cache(maxsize=1024)
+def _kv4_step(B, Hq, H, D, k, ps, max_prefix, dtype, scale, path, device):
+    """Descriptor of these sizes and its workspace bytes on `device`, the current one."""
+    desc = StepDesc(B, Hq, H, D, k, ps, max_prefix, dtype, scale, path)
+    return desc, step_attn_kv4_workspace_bytes(desc)
+
+
 def step_attn_kv4(q, k_blk, v_blk, cache, k, *, max_prefix_len, step_keys=True, append=True, scale=0.0,
                   path="auto", out=None, lse=None, want_lse=True, workspace=None, stream=None):
     """Three-zone step attention over a cache held in 4 bits.  ``append`` stores
     the draft rows too (quantised); ``step_keys=False`` attends the cache alone.
     Returns (out, lse)."""
+    if _away(q, "q", stream):
+        with _on(q.device, stream):
+            return step_attn_kv4(q, k_blk, v_blk, cache, k, max_prefix_len=max_prefix_len, step_keys=step_keys,
+                                 append=append, scale=scale, path=path, out=out, lse=lse, want_lse=want_lse,
+                                 workspace=workspace)
     _dev(q, "q")
-    dev = q.device
+    dev, dt = q.device, q.dtype
     if q.dim() != 4 or not isinstance(k_blk, torch.Tensor) or k_blk.dim() != 4:
         raise ValueError("q must be [B][R][Hq][D], k_blk and v_blk [B][R][Hkv][D]")
     B, R, Hq, D = q.shape
     H = k_blk.shape[2]
     if R != (1 if k == 0 else k + k * k):
         raise ValueError(f"q has {R} rows per sequence, k = {k} needs {1 if k == 0 else k + k * k}")
-    _shaped(k_blk, "k_blk", (B, R, H, D), q.dtype, dev)
-    _shaped(v_blk, "v_blk", (B, R, H, D), q.dtype, dev)
-    desc = step_attn_kv4_desc(q, k_blk, cache, k, max_prefix_len, scale, path)
-    cdesc = make_cache_desc(cache, dev)
-    if cache["k_pages"].shape[1] != H:
-        raise ValueError(f"the cache holds {cache['k_pages'].shape[1]} heads, k_blk {H}")
-    if cache["page_table"].shape[0] != B or cache["seq_lens"].shape[0] != B:
-        raise ValueError(f"the cache's table and lengths must be of {B} sequences")
+    _shaped(k_blk, "k_blk", (B, R, H, D), dt, dev)
+    _shaped(v_blk, "v_blk", (B, R, H, D), dt, dev)
+    ps = _kv4_page_size(cache, D, dev)
+    kp, table, lens = cache["k_pages"], cache["page_table"], cache["seq_lens"]
+    _dev(table, "page_table", torch.int32, dev)
+    _shaped(lens, "seq_lens", (B,), torch.int32, dev)
+    if kp.shape[1] != H:
+        raise ValueError(f"the cache holds {kp.shape[1]} heads, k_blk {H}")
+    if table.dim() != 2 or table.shape[0] != B:
+        raise ValueError(f"page_table is {tuple(table.shape)}, expected [{B}][max_pages]")
+    desc, need = _kv4_step(B, Hq, H, D, k, ps, int(max_prefix_len), _dtype_code(q), float(scale), _PATHS[path],
+                           dev.index)
+    cdesc = KVCacheDesc(kp.data_ptr(), cache["v_pages"].data_ptr(), table.data_ptr(), lens.data_ptr(), kp.shape[0],
+                        table.shape[1])
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _shaped(out, "out", q.shape, dt, dev)
+    if lse is not None:
+        _shaped(lse, "lse", (B, R, Hq), torch.float32, dev)
+    elif want_lse:
+        lse = q.new_empty((B, R, Hq), dtype=torch.float32)
+    if workspace is None and not need:
+        ws, wbytes = None, 0
+    else:
+        workspace, wbytes = _scratch(need, workspace, dev)
+        ws = workspace.data_ptr()
     flags = (PART_STEP_KEYS if step_keys else 0) | (PART_APPEND if append else 0)
-    with _launching(dev, stream) as s:
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = torch.empty((B, R, Hq), dtype=torch.float32, device=dev)
-        _shaped(out, "out", q.shape, q.dtype, dev)
-        if lse is not None:
-            _shaped(lse, "lse", (B, R, Hq), torch.float32, dev)
-        ws, wbytes = _scratch(step_attn_kv4_workspace_bytes(desc), workspace, dev)
-        st = lib().tidar_step_attn_kv4(ctypes.byref(desc), ctypes.byref(cdesc), _ptr(q), _ptr(k_blk), _ptr(v_blk),
-                                       flags, _ptr(out), _ptr(lse), _ptr(ws), wbytes, s)
-    _check(st, "tidar_step_attn_kv4")
+    st = lib().tidar_step_attn_kv4(ctypes.byref(desc), ctypes.byref(cdesc), q.data_ptr(), k_blk.data_ptr(),
+                                   v_blk.data_ptr(), flags, out.data_ptr(), None if lse is None else lse.data_ptr(), ws,
+                                   wbytes, _raw_stream(dev.index))
+    if st:
+        _check(st, "tidar_step_attn_kv4")
     return out, lse
 
 
@@ -938,25 +987,27 @@ def commit_kv4(cache, accept_count, k, *, head_dim, max_prefix_len, released=Non
                stream=None):
     """``commit`` for a cache held in 4 bits.  Returns (released, num_released)."""
     kp = cache["k_pages"]
-    _dev(kp, "k_pages", torch.uint8)
+    if _away(kp, "k_pages", stream):
+        with _on(kp.device, stream):
+            return commit_kv4(cache, accept_count, k, head_dim=head_dim, max_prefix_len=max_prefix_len,
+                              released=released, num_released=num_released)
     dev = kp.device
     ps = _kv4_page_size(cache, head_dim, dev)
     B, H, n = cache["seq_lens"].shape[0], kp.shape[1], max(k, 1)
-    desc = StepDesc(batch=B, num_q_heads=H, num_kv_heads=H, head_dim=head_dim, k=k, page_size=ps,
-                    max_prefix_len=int(max_prefix_len), dtype=BF16, softmax_scale=0.0, path=PATH_AUTO)
+    desc = StepDesc(B, H, H, head_dim, k, ps, int(max_prefix_len), BF16, 0.0, PATH_AUTO)
     cdesc = make_cache_desc(cache, dev)
     _shaped(accept_count, "accept_count", (B,), torch.int32, dev)
     cap = B * ((n + ps - 1) // ps + 1)
-    with _launching(dev, stream) as s:
-        if released is None:
-            released = torch.empty(cap, dtype=torch.int32, device=dev)
-        if num_released is None:
-            num_released = torch.empty(1, dtype=torch.int32, device=dev)
-        _shaped(released, "released", (cap,), torch.int32, dev)
-        _shaped(num_released, "num_released", (1,), torch.int32, dev)
-        st = lib().tidar_commit_kv4(ctypes.byref(desc), ctypes.byref(cdesc), _ptr(accept_count), _ptr(released),
-                                    _ptr(num_released), s)
-    _check(st, "tidar_commit_kv4")
+    if released is None:
+        released = accept_count.new_empty((cap,))
+    if num_released is None:
+        num_released = accept_count.new_empty((1,))
+    _shaped(released, "released", (cap,), torch.int32, dev)
+    _shaped(num_released, "num_released", (1,), torch.int32, dev)
+    st = lib().tidar_commit_kv4(ctypes.byref(desc), ctypes.byref(cdesc), accept_count.data_ptr(),
+                                released.data_ptr(), num_released.data_ptr(), _raw_stream(dev.index))
+    if st:
+        _check(st, "tidar_commit_kv4")
     return released, num_released
 
 
@@ -964,35 +1015,51 @@ def linear_fused_workspace_bytes(rows: int, out_features: int, in_features: int)
     return int(lib().tidar_linear_fused_workspace_bytes(int(rows), int(out_features), int(in_features)))
 
 
+@functools.lru_cache(maxsize=1024)
+def _linear_need(rows, N, K, device):
+    """Workspace bytes of these sizes on `device`, the current one."""
+    return linear_fused_workspace_bytes(rows, N, K)
+
+
 def linear_fused(x, w, *, bias=None, activation="none", residual=None, out=None, workspace=None, stream=None):
     """y = activation(x w^T + bias) + residual (bf16; x [..., in], w [out][in])
     on the tensor cores, rounded once.  ``activation``: none, relu, gelu (erf),
     gelu_tanh or silu.  ``residual`` has y's shape and may be ``out`` itself."""
+    if _away(x, "x", stream):
+        with _on(x.device, stream):
+            return linear_fused(x, w, bias=bias, activation=activation, residual=residual, out=out,
+                                workspace=workspace)
     _dev(x, "x", torch.bfloat16)
     dev = x.device
     _dev(w, "w", torch.bfloat16, dev)
     if w.dim() != 2 or x.dim() < 1 or x.shape[-1] != w.shape[1]:
         raise ValueError(f"x is {tuple(x.shape)}, w {tuple(w.shape)}: x must be [..., in], w [out][in]")
-    if activation not in ACTIVATIONS:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation is {activation!r}, expected one of {sorted(ACTIVATIONS)}")
     N, K = w.shape
     shape = (*x.shape[:-1], N)
-    rows = 1
-    for n in x.shape[:-1]:
-        rows *= n
+    rows = x.numel() // K if K else 0
     if bias is not None:
         _shaped(bias, "bias", (N,), torch.bfloat16, dev)
     if residual is not None:
         _shaped(residual, "residual", shape, torch.bfloat16, dev)
-    with _launching(dev, stream) as s:
-        if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        else:
-            _shaped(out, "out", shape, torch.bfloat16, dev)
-        ws, wbytes = _scratch(linear_fused_workspace_bytes(rows, N, K), workspace, dev)
-        st = lib().tidar_linear_fused(rows, N, K, BF16, _ptr(x), _ptr(w), _ptr(bias), ACTIVATIONS[activation],
-                                      _ptr(residual), _ptr(out), _ptr(ws), wbytes, s)
-    _check(st, "tidar_linear_fused")
+    if out is None:
+        out = x.new_empty(shape)
+    else:
+        _shaped(out, "out", shape, torch.bfloat16, dev)
+    need = _linear_need(rows, N, K, dev.index)
+    if workspace is None and not need:
+        ws, wbytes = None, 0
+    else:
+        workspace, wbytes = _scratch(need, workspace, dev)
+        ws = workspace.data_ptr()
+    st = lib().tidar_linear_fused(rows, N, K, BF16, x.data_ptr(), w.data_ptr(),
+                                  None if bias is None else bias.data_ptr(), act,
+                                  None if residual is None else residual.data_ptr(), out.data_ptr(), ws, wbytes,
+                                  _raw_stream(dev.index))
+    if st:
+        _check(st, "tidar_linear_fused")
     return out
 
 
@@ -1004,6 +1071,7 @@ def debug_set(knob: int, value: int) -> None:
     tensor-core attention's bounded waits run out; DEBUG_FORCE_SPLIT_PARTIALS
     sends key splits through workspace partials instead of the on-chip merge."""
     _check(lib().tidar_debug_set(knob, int(value)), "tidar_debug_set")
+    _kv4_step.cache_clear()                  # it may change the split count
 
 
 def device_status(stream=None) -> tuple[int, int]:
