@@ -170,7 +170,8 @@ Plan make_plan(const tidar_step_desc* d, int path, bool kv4 = false) {
   // (decode path), 1 block for SIMT
   const int max_ns = path == 3 ? ((maxP + 63) / 64 / 2 > 0 ? (maxP + 63) / 64 / 2 : 1)
                                : ((path == 2 || path == 4) ? (blocks128 / 2 > 0 ? blocks128 / 2 : 1)
-                                                           : (blocks128 > 0 ? blocks128 : 1));
+                                                           : kv4 ? ((maxP + 31) / 32 > 0 ? (maxP + 31) / 32 : 1)
+                                                                 : (blocks128 > 0 ? blocks128 : 1));
   auto split_keys = [&](int n) {
     if (path == 3) {                                  // pages of 64 keys
       const int pages = (maxP + 63) / 64;
@@ -178,6 +179,15 @@ Plan make_plan(const tidar_step_desc* d, int path, bool kv4 = false) {
       p.keys_per_split = (pps > 0 ? pps : 1) * 64;
       p.nsplit = maxP > 0 ? (maxP + p.keys_per_split - 1) / p.keys_per_split : 1;
       if (p.nsplit < 1) p.nsplit = 1;
+      return;
+    }
+    if (path == 1 && kv4) {
+      // 4-bit cache on the CUDA cores: splits in steps of 32 keys (a warp walks
+      // its keys eight at a time, so a short split is what a small call costs:
+      // the tiny fp32 step takes 62 us with splits of 128 keys, 21 with 32)
+      const int steps = (maxP + 31) / 32, per = (steps + n - 1) / n;
+      p.keys_per_split = (per > 0 ? per : 1) * 32;
+      p.nsplit = maxP > 0 ? (maxP + p.keys_per_split - 1) / p.keys_per_split : 1;
       return;
     }
     // tensor-core paths: the last split also runs the tile's step-key windows

@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
     const int ns = a.nsplit, rank = (int)cluster_rank();
     cluster_sync_all();
     const int owned = prm.M > rank ? (prm.M - rank + ns - 1) / ns : 0;
-    tc05::merge_rows<1, 8>(ost, lst, ns, rank, owned, out_row, out, a.lse_out);
+    tc05::merge_rows<1, 8, true>(ost, lst, ns, rank, owned, out_row, out, a.lse_out);
     cluster_sync_all();
   } else {
     const long long stride = (long long)a.B * a.R * a.Hq;
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(Kv4Shape<NT>::kThreads, 1) attn_kv4_dec_kernel
       for (int G = 0; G < 4; ++G) load_vec<__nv_bfloat16, 8>(src + 32 * G, x[G]);
       uint8_t* base = static_cast<uint8_t*>(const_cast<void*>(is_key ? a.k_pages : a.v_pages)) +
                       ((size_t)(mapped ? page : 0) * a.Hkv + g_head) * kv4_page_bytes(ps, 128);
-      kv4_store_quad<128>(x, is_key, base, ps, pos % ps, in && mapped);
+      kv4_store_quad<128, true>(x, is_key, base, ps, pos % ps, in && mapped);
     }
   }
 }

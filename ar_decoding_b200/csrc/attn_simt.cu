@@ -157,12 +157,14 @@ __global__ void __launch_bounds__(kWarps * 32) attn_simt_kernel(AttnArgs a) {
     }
   }
 
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  // KV4: a NaN among the keys' values makes the row NaN, merged or not
+  const bool any = KV4 ? l != 0.f : l > 0.f;
+  const float inv = any ? 1.f / l : 0.f;
   float o[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) o[i] = acc[i] * inv;
   const size_t row = (size_t)(b * a.R + rho) * a.Hq + h;
-  const float lse = l > 0.f ? mx + logf(l) : -INFINITY;
+  const float lse = any ? mx + logf(l) : -INFINITY;
   if (a.nsplit == 1) {
     store_vec<T, VPL>(static_cast<T*>(a.out) + row * D + lane * VPL, o);
     if (a.lse_out && lane == 0) a.lse_out[row] = lse;
@@ -218,17 +220,18 @@ __global__ void __launch_bounds__(kWarps * 32) finalize_kernel(AttnArgs a, int m
       for (int u = 0; u < kFinChunk; ++u) {
         const int sp = s0 + u;
         const float w = __shfl_sync(0xffffffffu, sp < 32 ? wa : wb, sp & 31);
-        if (sp < ns && w > 0.f) {
+        if (sp < ns && (KV4 ? w != 0.f : w > 0.f)) {
 #pragma unroll
           for (int i = 0; i < VPL; ++i) acc[i] = fmaf(w, v[u][i], acc[i]);
         }
       }
     }
-    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    const bool any = KV4 ? wsum != 0.f : wsum > 0.f;
+    const float inv = any ? 1.f / wsum : 0.f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) acc[i] *= inv;
     store_vec<T, VPL>(static_cast<T*>(a.out) + row * D + lane * VPL, acc);
-    if (a.lse_out && lane == 0) a.lse_out[row] = wsum > 0.f ? mx + logf(wsum) : -INFINITY;
+    if (a.lse_out && lane == 0) a.lse_out[row] = any ? mx + logf(wsum) : -INFINITY;
     return;
   }
   // draft-row append: one block per (b, r)
@@ -258,7 +261,7 @@ __global__ void __launch_bounds__(kWarps * 32) finalize_kernel(AttnArgs a, int m
         for (int e = 0; e < 8; ++e) x[G][e] = to_f32(src[32 * G + 8 * y + e]);
       uint8_t* base = static_cast<uint8_t*>(const_cast<void*>(is_key ? a.k_pages : a.v_pages)) +
                       ((size_t)page * a.Hkv + g) * kv4_page_bytes(a.page_size, D);
-      kv4_store_quad<D>(x, is_key, base, a.page_size, pos % a.page_size, live);
+      kv4_store_quad<D, sizeof(T) == 2>(x, is_key, base, a.page_size, pos % a.page_size, live);
     }
     return;
   }

@@ -359,7 +359,7 @@ __device__ __forceinline__ void append_kv4(const AttnArgs& a, const int32_t* tab
     for (int G = 0; G < 4; ++G) load_vec<__nv_bfloat16, 8>(src + 32 * G, x[G]);
     uint8_t* base = static_cast<uint8_t*>(const_cast<void*>(is_key ? a.k_pages : a.v_pages)) +
                     ((size_t)(mapped ? page : 0) * a.Hkv + g) * kv4_page_bytes(ps, 128);
-    kv4_store_quad<128>(x, is_key, base, ps, pos % ps, in && mapped);
+    kv4_store_quad<128, true>(x, is_key, base, ps, pos % ps, in && mapped);
   }
 }
 
@@ -851,9 +851,10 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_q, const CUtenso
     const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - mt);
     const float f1 = (m1 == -INFINITY || nb1 == 0) ? 0.f : ex2(m1 - mt);
     const float lt = l0 * f0 + l1 * f1;
-    const float inv = lt > 0.f ? 1.f / lt : 0.f;
+    const bool any = KV4 ? lt != 0.f : lt > 0.f;         // KV4: a NaN sum stays one
+    const float inv = any ? 1.f / lt : 0.f;
     const float g0 = f0 * inv, g1 = f1 * inv;
-    const float lse = lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+    const float lse = any ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
     const bool write = r < rows_valid && ok;
     const int col0 = 32 * (2 * t + hf);                  // this thread's 32 output columns
     {
@@ -928,7 +929,7 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_q, const CUtenso
     cluster_sync_all();
     if (threadIdx.x == 0) { TIDAR_TRACE_AT(1540); TIDAR_TRACE_CTA(3); }
     const int owned = rows_valid > rank ? (rows_valid - rank + ns - 1) / ns : 0;
-    merge_rows<4, 2>(ost, lst, ns, rank, owned, out_row, static_cast<__nv_bfloat16*>(a.out), a.lse_out);
+    merge_rows<4, 2, KV4>(ost, lst, ns, rank, owned, out_row, static_cast<__nv_bfloat16*>(a.out), a.lse_out);
     if (threadIdx.x == 0) TIDAR_TRACE_AT(1541);
     cluster_sync_all();
   } else {

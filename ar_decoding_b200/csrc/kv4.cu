@@ -20,6 +20,8 @@ constexpr int kQThreads = 256;
 
 struct Kv4RowsArgs {
   int rows, Hkv, ps;
+  uint32_t units;              // rows * 2 Hkv, below 2^31
+  uint32_t div_mul, div_shift; // u / (2 Hkv) = (u div_mul >> 32) >> div_shift for u < 2^31
   long long nslots;            // num_pages * page_size
   long long k_stride, v_stride;  // elements between rows of k / v
   void* k;
@@ -61,24 +63,24 @@ __global__ void __launch_bounds__(kQThreads) kv4_rows_kernel(Kv4RowsArgs a) {
   constexpr int N = D / 32;
   pdl_wait();
   pdl_trigger();
-  const long long units = (long long)a.rows * 2 * a.Hkv;       // (row, K or V, head)
-  const long long step = (long long)gridDim.x * (kQThreads / 4);
-  const int y = (int)threadIdx.x & 3;
+  const int y = (int)threadIdx.x & 3, lps = 31 - __clz(a.ps);
+  const size_t page_bytes = kv4_page_bytes(a.ps, D);
   bool bad = false;
-  // whole warps loop: the eight quads of a warp take neighbouring units
-  for (long long u0 = (long long)blockIdx.x * (kQThreads / 4) + (threadIdx.x >> 5) * 8; u0 < units; u0 += step) {
-    const long long u = u0 + ((threadIdx.x & 31) >> 2);
-    const bool in = u < units;
-    const int row = in ? (int)(u / (2 * a.Hkv)) : 0;
-    const int hv = in ? (int)(u % (2 * a.Hkv)) : 0;
+  // A unit is one row of one head of K or V, four lanes; heads fastest, so the
+  // eight units of a warp are neighbours in the row tensors.  Whole warps loop.
+  for (uint32_t u0 = blockIdx.x * (kQThreads / 4) + (threadIdx.x >> 5) * 8; u0 < a.units; u0 += gridDim.x * (kQThreads / 4)) {
+    const uint32_t u = u0 + ((threadIdx.x & 31) >> 2);
+    const bool in = u < a.units;
+    const uint32_t row = in ? __umulhi(u, a.div_mul) >> a.div_shift : 0u;   // u / (2 Hkv)
+    const int hv = in ? (int)(u - row * 2u * (uint32_t)a.Hkv) : 0;
     const bool is_key = hv < a.Hkv;
     const int head = is_key ? hv : hv - a.Hkv;
     const long long slot = in ? a.slots[row] : -1;
     const bool live = slot >= 0 && slot < a.nslots;
     if (slot >= a.nslots) bad = true;
-    const long long page = live ? slot / a.ps : 0;
-    const int r = live ? (int)(slot % a.ps) : 0;
-    uint8_t* base = (is_key ? a.k_pages : a.v_pages) + (size_t)(page * a.Hkv + head) * kv4_page_bytes(a.ps, D);
+    const long long page = live ? slot >> lps : 0;
+    const int r = live ? (int)slot & (a.ps - 1) : 0;
+    uint8_t* base = (is_key ? a.k_pages : a.v_pages) + (size_t)(page * a.Hkv + head) * page_bytes;
     T* p = static_cast<T*>(is_key ? a.k : a.v) + (size_t)row * (is_key ? a.k_stride : a.v_stride) +
            (size_t)head * D + 8 * y;
     float x[N][8];
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(kQThreads) kv4_rows_kernel(Kv4RowsArgs a) {
           for (int e = 0; e < 8; ++e) x[G][e] = 0.f;
         }
       }
-      kv4_store_quad<D>(x, is_key, base, a.ps, r, live);
+      kv4_store_quad<D, sizeof(T) == 2>(x, is_key, base, a.ps, r, live);
     } else if (live) {
       uint32_t w[N];
       float s[N];
@@ -114,8 +116,7 @@ __global__ void __launch_bounds__(kQThreads) kv4_rows_kernel(Kv4RowsArgs a) {
 
 template <bool kStore>
 cudaError_t launch_rows(const Kv4RowsArgs& a, int D, bool bf16, cudaStream_t s) {
-  const long long units = (long long)a.rows * 2 * a.Hkv;
-  const int grid = (int)std::min<long long>((units + kQThreads / 4 - 1) / (kQThreads / 4), 148 * 64);
+  const int grid = (int)std::min<uint32_t>((a.units + kQThreads / 4 - 1) / (kQThreads / 4), 148 * 64);
   auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), kQThreads, 0, s, a); };
   if (bf16) return D == 64 ? go(kv4_rows_kernel<__nv_bfloat16, 64, kStore>) : go(kv4_rows_kernel<__nv_bfloat16, 128, kStore>);
   return D == 64 ? go(kv4_rows_kernel<float, 64, kStore>) : go(kv4_rows_kernel<float, 128, kStore>);
@@ -140,6 +141,16 @@ tidar_status prepare(const tidar_kv4_desc* d, const void* k_pages, const void* v
   a.v_stride = d->v_row_stride ? d->v_row_stride : row;
   const int per16 = d->dtype == TIDAR_F32 ? 4 : 8;
   if (a.k_stride < row || a.v_stride < row || a.k_stride % per16 || a.v_stride % per16) return TIDAR_ERR_INVALID_ARG;
+  if (d->num_kv_heads > (1 << 24) || (long long)d->rows * 2 * d->num_kv_heads >= (1LL << 31)) return TIDAR_ERR_UNSUPPORTED;
+  // Division by n = 2 Hkv: with 2^l >= n > 2^(l-1) and m = ceil(2^(31+l) / n),
+  // floor(u m / 2^(31+l)) = floor(u / n) for every u < 2^31 (m n - 2^(31+l) < n <=
+  // 2^l, so u times the excess stays below 2^(31+l)); m < 2^32.
+  const uint32_t n = 2u * (uint32_t)d->num_kv_heads;
+  uint32_t l = 1;
+  while ((1u << l) < n) ++l;
+  a.units = (uint32_t)d->rows * n;
+  a.div_mul = (uint32_t)(((1ULL << (31 + l)) + n - 1) / n);
+  a.div_shift = l - 1;
   a.rows = d->rows; a.Hkv = d->num_kv_heads; a.ps = d->page_size;
   a.nslots = (long long)d->num_pages * d->page_size;
   a.k = const_cast<void*>(k); a.v = const_cast<void*>(v); a.slots = slots;

@@ -49,25 +49,39 @@ __device__ __forceinline__ float kv4_scale(uint32_t top) {
   return __uint_as_float(b);
 }
 
-// Nearest integer to x / s, ties to even.  c = rint(x (1/s)) is off by at most
-// one, next to a tie; the remainder x - c s is exact (c s has 8 bits), so the
-// comparison with s/2 decides.
-__device__ __forceinline__ int kv4_code(float x, float s, float rs) {
-  const float c = rintf(x * rs);
-  const float r = fmaf(-c, s, x), h = 0.5f * s;
-  int k = (int)c;
-  if (fabsf(r) > h || (fabsf(r) == h && (k & 1))) k += r > 0.f ? 1 : -1;
-  return k;
+// Nearest integer to x / s, ties to even, in the low bits of the result (two's
+// complement).  Adding 1.5 2^23 rounds to an integer whose bits are the low
+// mantissa bits.
+//   bf16 x: q = x / s correctly rounded (one Newton step on x (1/s): the
+//     correction is within a few percent of what it has to be, so a quotient
+//     that is representable comes out exactly).  x and s have 8 and 5 bits, so a
+//     quotient that is no tie is 2^-13 away from one and stays so.
+//   fp32 x: c = round(x (1/s)) is off by at most one, next to a tie; the
+//     remainder x - c s is exact, and its comparison with s/2 decides.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t kv4_code(float x, float s, float rs) {
+  constexpr float kRound = 12582912.f;
+  if constexpr (kBf16) {
+    const float q = x * rs;
+    return __float_as_uint(__fadd_rn(fmaf(fmaf(-q, s, x), rs, q), kRound));
+  } else {
+    const float t = __fadd_rn(x * rs, kRound), c = t - kRound;
+    const float r = fmaf(-c, s, x), h = 0.5f * s;
+    uint32_t k = __float_as_uint(t);
+    if (fabsf(r) > h || (fabsf(r) == h && (k & 1u))) k += r > 0.f ? 1u : ~0u;
+    return k;
+  }
 }
 
 // Eight dims of one group (dims 8y .. 8y+7) as a key-row word: units 2G (even
 // dims) and 2G + 1 (odd dims).
+template <bool kBf16>
 __device__ __forceinline__ uint32_t kv4_pack8(const float (&x)[8], float s) {
   if (!(s > 0.f)) return 0u;                       // scale 0 or NaN
   const float rs = __frcp_rn(s);
   uint32_t w = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w |= (uint32_t)(kv4_code(x[e], s, rs) & 15) << (4 * (e >> 1) + 16 * (e & 1));
+  for (int e = 0; e < 8; ++e) w |= (kv4_code<kBf16>(x[e], s, rs) & 15u) << (4 * (e >> 1) + 16 * (e & 1));
   return w;
 }
 
@@ -107,8 +121,8 @@ __device__ __forceinline__ __nv_bfloat162 kv4_codes2(uint32_t w, int i) {
 // Quantise and store one row of one head: four consecutive lanes (y = lane & 3)
 // each bring the dims 32G + 8y + e, e < 8, of every group G in x[G][e] and
 // write chunk y.  All 32 lanes call it; a quad with live = false writes
-// nothing.  base: the page's bytes of this head.
-template <int D>
+// nothing.  base: the page's bytes of this head; kBf16: the values are bf16.
+template <int D, bool kBf16>
 __device__ __forceinline__ void kv4_store_quad(const float (&x)[D / 32][8], bool is_key, uint8_t* base, int ps, int r,
                                                bool live) {
   constexpr int N = D / 32;
@@ -124,7 +138,7 @@ __device__ __forceinline__ void kv4_store_quad(const float (&x)[D / 32][8], bool
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const float s = kv4_scale(top);
     sc[G] = __float_as_uint(s) >> 16;              // exact: 5 significant bits
-    w[G] = kv4_pack8(x[G], s);
+    w[G] = kv4_pack8<kBf16>(x[G], s);
   }
   if (!live) return;
   uint32_t o[N];

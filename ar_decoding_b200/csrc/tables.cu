@@ -32,7 +32,7 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kTThreads = 512;
+constexpr int kTThreads = 1024;
 constexpr int kTWarps = kTThreads / 32;
 constexpr int kTMaxCluster = 8;           // portable
 constexpr int kTablesMaxBatch = 65536;
@@ -73,31 +73,37 @@ __global__ void __launch_bounds__(kTThreads) tables_kernel(TablesArgs a, int per
   pdl_wait();
   pdl_trigger();
 
-  // 1. validate and count, one warp per sequence
+  const int count = *a.free_count;
+  // 1. validate and count, one warp per sequence; the row is copied on the way
+  //    (an update in place has nothing to copy: only the entries it needs are
+  //    read), eight entries a lane in flight
   for (int i = wid; i < nown; i += kTWarps) {
     const int b = b0 + i;
     const int c = a.ctx[b], m = a.newl[b];
+    const int32_t* src = a.table_in + (size_t)b * a.max_pages;
+    int32_t* dst = a.table_out + (size_t)b * a.max_pages;
+    const bool copy = src != dst;
     const bool len_ok = c >= 0 && m >= 0 && (long long)c + m <= (long long)a.max_pages * ps;
     if (!len_ok && lane == 0) raise_error(a.err, TIDAR_DEVERR_BAD_LEN);
+    const bool rows = len_ok && m > 0;
+    const int lo = rows ? c / ps : 0, first = rows ? (int)(((long long)c + ps - 1) / ps) : 0;
+    const int last = rows ? (int)(((long long)c + m + ps - 1) / ps) : 0;
     int need = 0;
     bool bad = false;
-    if (len_ok && m > 0) {
-      const int32_t* row = a.table_in + (size_t)b * a.max_pages;
-      const int first = (int)(((long long)c + ps - 1) / ps), last = (int)(((long long)c + m + ps - 1) / ps);
-      for (int e0 = c / ps; e0 < last; e0 += 128) {
-        int id[4];
+    for (int e0 = copy ? 0 : lo; e0 < (copy ? a.max_pages : last); e0 += 256) {
+      int id[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int e = e0 + 32 * u + lane;
-          id[u] = e < last ? row[e] : 0;
-        }
+      for (int u = 0; u < 8; ++u) {
+        const int e = e0 + 32 * u + lane;
+        id[u] = e < (copy ? a.max_pages : last) ? src[e] : 0;
+      }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int e = e0 + 32 * u + lane;
-          const bool in = e < last, want = in && e >= first && id[u] == -1;
-          bad = bad || (in && !want && (id[u] < 0 || id[u] >= a.num_pages));
-          need += __popc(__ballot_sync(0xffffffffu, want));
-        }
+      for (int u = 0; u < 8; ++u) {
+        const int e = e0 + 32 * u + lane;
+        if (copy && e < a.max_pages) dst[e] = id[u];
+        const bool in = e >= lo && e < last, want = in && e >= first && id[u] == -1;
+        bad = bad || (in && !want && (id[u] < 0 || id[u] >= a.num_pages));
+        need += __popc(__ballot_sync(0xffffffffu, want));
       }
     }
     bad = __any_sync(0xffffffffu, bad);
@@ -148,7 +154,6 @@ __global__ void __launch_bounds__(kTThreads) tables_kernel(TablesArgs a, int per
     all_r += x;
     all_n += y;
   }
-  const int count = *a.free_count;
   const bool pool_ok = count >= 0 && count <= a.capacity && all_n <= count;
   const bool ok = pool_ok && all_r <= a.max_rows;
   cl.sync();                     // no CTA leaves, or rewrites the count, while a peer reads
@@ -158,33 +163,31 @@ __global__ void __launch_bounds__(kTThreads) tables_kernel(TablesArgs a, int per
     *a.count_out = ok ? count - (int)all_n : count;
     a.starts[a.B] = (int32_t)min(all_r, (long long)a.max_rows);
   }
-  // 4. the table rows and the starts (a start past the token buffer is its end)
+  // 4. the starts (one past the token buffer is its end) and the popped pages
   for (int i = wid; i < nown; i += kTWarps) {
     const int b = b0 + i;
     const TabRec r = rec[i];
     if (lane == 0) a.starts[b] = (int32_t)min(base_r + r.rows, (long long)a.max_rows);
+    const long long pages = (i + 1 < nown ? rec[i + 1].need : s_need) - r.need;
+    if (!ok || pages == 0) continue;
     const int c = a.ctx[b], m = a.newl[b];
     const int32_t* src = a.table_in + (size_t)b * a.max_pages;
     int32_t* dst = a.table_out + (size_t)b * a.max_pages;
-    const bool fill = ok && r.ok && m > 0;
-    const int first = fill ? (int)(((long long)c + ps - 1) / ps) : a.max_pages;
-    const int last = fill ? (int)(((long long)c + m + ps - 1) / ps) : 0;
+    const int first = (int)(((long long)c + ps - 1) / ps), last = (int)(((long long)c + m + ps - 1) / ps);
     long long pop = base_n + r.need;              // pages popped before this entry
-    for (int e0 = 0; e0 < a.max_pages; e0 += 128) {
-      int id[4];
+    for (int e0 = first; e0 < last; e0 += 256) {
+      int id[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 8; ++u) {
         const int e = e0 + 32 * u + lane;
-        id[u] = e < a.max_pages ? src[e] : 0;
+        id[u] = e < last ? src[e] : 0;
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int e = e0 + 32 * u + lane;
-        const bool want = e >= first && e < last && id[u] == -1;
+      for (int u = 0; u < 8; ++u) {
+        const bool want = id[u] == -1;            // 0 past the end
         const unsigned m32 = __ballot_sync(0xffffffffu, want);
-        if (want) id[u] = a.free_pages[count - 1 - (pop + __popc(m32 & ((1u << lane) - 1u)))];
+        if (want) dst[e0 + 32 * u + lane] = a.free_pages[count - 1 - (pop + __popc(m32 & ((1u << lane) - 1u)))];
         pop += __popc(m32);
-        if (e < a.max_pages && (want || dst != src)) dst[e] = id[u];
       }
     }
   }

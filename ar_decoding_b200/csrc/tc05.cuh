@@ -297,7 +297,7 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
                : "memory");
   return v;
 }
-template <int U, int NC, class RowOf>
+template <int U, int NC, bool kNan, class RowOf>
 __device__ __forceinline__ void merge_rows_t(const float* ost, const float* lst, int ns, int rank, int owned,
                                              RowOf out_row, __nv_bfloat16* out, float* lse_out) {
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31, nw = (int)blockDim.x >> 5;
@@ -356,7 +356,7 @@ __device__ __forceinline__ void merge_rows_t(const float* ost, const float* lst,
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const float ws = __shfl_sync(kAll, w[u], (s0 + j) & 31);
-          if (s0 + j < ns && ws > 0.f) {
+          if (s0 + j < ns && (kNan ? ws != 0.f : ws > 0.f)) {
             acc[u].x = fmaf(ws, x[u][j].x, acc[u].x); acc[u].y = fmaf(ws, x[u][j].y, acc[u].y);
             acc[u].z = fmaf(ws, x[u][j].z, acc[u].z); acc[u].w = fmaf(ws, x[u][j].w, acc[u].w);
           }
@@ -366,28 +366,30 @@ __device__ __forceinline__ void merge_rows_t(const float* ost, const float* lst,
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (orow[u] < 0) continue;
-      const float inv = wsum[u] > 0.f ? 1.f / wsum[u] : 0.f;
+      const bool any = kNan ? wsum[u] != 0.f : wsum[u] > 0.f;
+      const float inv = any ? 1.f / wsum[u] : 0.f;
       uint2 o;
       o.x = cvt_bf16x2(acc[u].x * inv, acc[u].y * inv);
       o.y = cvt_bf16x2(acc[u].z * inv, acc[u].w * inv);
       *reinterpret_cast<uint2*>(out + orow[u] * 128 + 4 * lane) = o;
       if (lane == 0 && lse_out)
-        lse_out[orow[u]] = wsum[u] > 0.f ? (mx[u] + log2f(wsum[u])) * 0.69314718055994531f : -INFINITY;
+        lse_out[orow[u]] = any ? (mx[u] + log2f(wsum[u])) * 0.69314718055994531f : -INFINITY;
     }
   }
 }
 
 // This CTA's share of the merge: U rows per warp (at most kMaxU), NC splits'
 // rows in flight per chunk, U picked so that the block's warps take all
-// `owned` rows in one pass where they can (ns <= 32).
-template <int kMaxU, int NC, class RowOf>
+// `owned` rows in one pass where they can (ns <= 32).  kNan: a split whose lse is
+// NaN makes the row NaN (else it gets no weight).
+template <int kMaxU, int NC, bool kNan = false, class RowOf>
 __device__ __forceinline__ void merge_rows(const float* ost, const float* lst, int ns, int rank, int owned,
                                            RowOf out_row, __nv_bfloat16* out, float* lse_out) {
   const int nw = (int)blockDim.x >> 5;
   const int per = (owned + nw - 1) / nw;
-  if (per <= 1 || kMaxU == 1) merge_rows_t<1, NC>(ost, lst, ns, rank, owned, out_row, out, lse_out);
-  else if (per <= 2 || kMaxU == 2) merge_rows_t<2, NC>(ost, lst, ns, rank, owned, out_row, out, lse_out);
-  else merge_rows_t<4, NC>(ost, lst, ns, rank, owned, out_row, out, lse_out);
+  if (per <= 1 || kMaxU == 1) merge_rows_t<1, NC, kNan>(ost, lst, ns, rank, owned, out_row, out, lse_out);
+  else if (per <= 2 || kMaxU == 2) merge_rows_t<2, NC, kNan>(ost, lst, ns, rank, owned, out_row, out, lse_out);
+  else merge_rows_t<4, NC, kNan>(ost, lst, ns, rank, owned, out_row, out, lse_out);
 }
 
 }  // namespace tc05

@@ -529,7 +529,8 @@ tidar_status tidar_build_tables(const tidar_tables_desc* desc, const int32_t* pa
  *   slots[row] = page * page_size + row in page, as tidar_build_tables writes
  *   them.  A negative slot skips its row, one past the cache does so with
  *   BAD_PAGE.  The slots of a call must differ (else the content of a slot
- *   named twice is unspecified).
+ *   named twice is unspecified).  TIDAR_ERR_UNSUPPORTED when rows * 2 *
+ *   num_kv_heads >= 2^31 (both calls).
  * tidar_kv4_gather: the values of the rows at `slots`, exact in either dtype;
  *   rows whose slot is negative or past the cache are left as they were.
  * tidar_step_attn_kv4: tidar_step_attn_part over such a cache: flags as there

@@ -204,6 +204,28 @@ def test_nan_and_infinite_rows_reach_their_sequence_only():
         compare(st, out, lse, seqs=[0])
 
 
+@pytest.mark.parametrize("force", [0, 1])
+@pytest.mark.parametrize("k", [0, 4])
+def test_nan_survives_the_merge_of_splits(k, force):
+    st = make(41, [4096, 4096], 8, 2, 128, k, 64, "bf16")
+    page = int(st["table"][1, 20])
+    st["cache"]["v_pages"][page, 1, 64 * 64 + 1] = 0x7f             # a value scale of row 0, head 1, first group: a NaN
+    st["cache"]["v_pages"][page, 1, 64 * 64] = 0xc0
+    page = int(st["table"][0, 40])
+    st["cache"]["k_pages"][page, 0, 64 * 64 + 1] = 0x7f             # a key scale of head 0
+    st["cache"]["k_pages"][page, 0, 64 * 64] = 0xc0
+    tidar.debug_set(tidar.DEBUG_FORCE_SPLIT_PARTIALS, force)
+    try:
+        for path in paths(k, 4, 128, "bf16"):
+            out, lse = run(st, path, append=False)
+            nan = torch.isnan(out)
+            assert nan[1, :, 4:, :32].all() and not nan[1, :, 4:, 32:].any() and not nan[1, :, :4].any(), path
+            assert nan[0, :, :4].all() and torch.isnan(lse[0, :, :4]).all() and not nan[0, :, 4:].any(), path
+            assert not torch.isnan(lse[1]).any() and not torch.isnan(lse[0, :, 4:]).any(), path
+    finally:
+        tidar.debug_set(tidar.DEBUG_FORCE_SPLIT_PARTIALS, 0)
+
+
 def test_device_errors_skip_their_work():
     for k in (0, 4):
         for path in paths(k, 4, 128, "bf16"):
