@@ -775,16 +775,21 @@ def build_tables(page_table, ctx_lens, new_lens, pool, *, page_size, num_pages, 
     max_rows = int(max_rows)
     if max_rows < 0:
         raise ValueError(f"max_rows is {max_rows}")
-    if out is None:
-        out = {}
-    new = page_table.new_empty
-    tab, cnt, sta, slo, pos = (out.get(n) for n in ("page_table", "free_count", "row_starts", "slots", "positions"))
-    tab = new((B, width)) if tab is None else tab
-    cnt = new((1,)) if cnt is None else cnt
-    sta = new((B + 1,)) if sta is None else sta
-    slo = new((max_rows,), dtype=torch.int64) if slo is None else slo
-    pos = new((max_rows,)) if pos is None else pos
-    if out:
+    if not out:
+        # one allocation of the int32 results (positions first: 8-byte aligned)
+        pos, tab, cnt, sta = page_table.new_empty((max_rows + B * width + B + 2,)).split(
+            (max_rows, B * width, 1, B + 1))
+        tab = tab.view(B, width)
+        slo = page_table.new_empty((max_rows,), dtype=torch.int64)
+    else:
+        new = page_table.new_empty
+        tab, cnt, sta, slo, pos = (out.get(n) for n in ("page_table", "free_count", "row_starts", "slots",
+                                                        "positions"))
+        tab = new((B, width)) if tab is None else tab
+        cnt = new((1,)) if cnt is None else cnt
+        sta = new((B + 1,)) if sta is None else sta
+        slo = new((max_rows,), dtype=torch.int64) if slo is None else slo
+        pos = new((max_rows,)) if pos is None else pos
         _shaped(tab, "page_table", (B, width), torch.int32, dev)
         _shaped(cnt, "free_count", (1,), torch.int32, dev)
         _shaped(sta, "row_starts", (B + 1,), torch.int32, dev)

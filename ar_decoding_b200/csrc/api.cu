@@ -219,7 +219,11 @@ Plan make_plan(const tidar_step_desc* d, int path, bool kv4 = false) {
   // waves count the clusters that can be resident at once.
   // A launch that already fills the device (units >= one wave) keeps one split:
   // with ragged batches the longest sequence, not the wave count, sets its time.
-  constexpr double kFixedBlocks = 3.0, kFinalizeBlocks = 2.0, kClusterMergeBlocks = 1.0;
+  // 4-bit decode: a block of 128 keys takes less, so the second launch weighs more
+  // (one 8192-key sequence: 10 splits merged on chip 10.7 us of kernel and one
+  // launch, 16 through partials 9.3 us and two).
+  constexpr double kFixedBlocks = 3.0, kClusterMergeBlocks = 1.0;
+  const double kFinalizeBlocks = kv4 && path == 3 ? 3.5 : 2.0;
   double best = 1e300;
   int best_n = 1;
   bool best_cluster = false;
