@@ -278,9 +278,9 @@ __device__ __forceinline__ long long block_scan(long long v, long long* ws, long
   return v + before;
 }
 
-// Index of the last of n non-decreasing values that is <= x (values[0] <= x).
-__device__ __forceinline__ int last_at_most(const int* values, int n, int x) {
-  int lo = 0, hi = n - 1;
+// Index in lo .. hi of the last of non-decreasing values that is <= x
+// (values[lo] <= x).
+__device__ __forceinline__ int last_at_most(const int* values, int lo, int hi, int x) {
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (values[mid] <= x) lo = mid;
@@ -291,7 +291,8 @@ __device__ __forceinline__ int last_at_most(const int* values, int n, int x) {
 
 // Shared memory: [B] first entry in use, [B] first entry that may be popped (-1:
 // the sequence is skipped), [B + 1] offsets of the sequences' entries, [B + 1]
-// row starts, [B] ctx, then the entries.
+// row starts, [B] ctx, a word per 32 entries (which of them need a page) and the
+// number of those before it, then the entries.
 __global__ void __launch_bounds__(kFThreads) fused_kernel(TablesArgs a, int entry_cap) {
   extern __shared__ __align__(16) unsigned char s_raw[];
   __shared__ long long ws[kFWarps];
@@ -300,12 +301,17 @@ __global__ void __launch_bounds__(kFThreads) fused_kernel(TablesArgs a, int entr
   int* s_off = s_first + a.B;
   int* s_start = s_off + a.B + 1;
   int* s_ctx = s_start + a.B + 1;
-  int* s_ent = s_ctx + a.B;
+  const int words = (entry_cap + 31) / 32;
+  unsigned* s_mask = reinterpret_cast<unsigned*>(s_ctx + a.B);
+  int* s_pre = reinterpret_cast<int*>(s_mask + words);
+  int* s_ent = s_pre + words;
+  __shared__ int s_bad;
   const int lps = 31 - __clz(a.ps), t = threadIdx.x;
   const bool lead = blockIdx.x == 0;
   pdl_wait();
   pdl_trigger();
-  const int count = *a.free_count;
+  const int count = *a.free_count, lane = t & 31;
+  if (t == 0) s_bad = 0;
   // 1. lengths: rows and entries in use of up to two sequences a thread
   constexpr int kPer = kFusedBatch / kFThreads;
   long long rows[kPer], used[kPer], rsum = 0, usum = 0;
@@ -343,35 +349,52 @@ __global__ void __launch_bounds__(kFThreads) fused_kernel(TablesArgs a, int entr
   const int total = (int)min(all_r, (long long)a.max_rows), ents = (int)min(all_u, (long long)entry_cap);
   if (t == 0) s_start[a.B] = total, s_off[a.B] = ents;
   __syncthreads();
-  // 2. the entries in use; a bad one skips its sequence
-  const int per = (ents + kFThreads - 1) / kFThreads;      // a contiguous run per thread, for the sums
-  for (int e = t; e < ents; e += kFThreads) {
-    const int b = last_at_most(s_off, a.B, e), at = s_lo[b] + e - s_off[b];
-    const int id = a.table_in[(size_t)b * a.max_pages + at];
-    s_ent[e] = id;
-    const bool want = id == -1 && at >= s_first[b];
-    if (!want && (id < 0 || id >= a.num_pages)) {
-      s_first[b] = 0x7fffffff;                             // every thread that writes it writes this
-      if (lead) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
+  // 2. the entries in use, and which need a page; a bad one skips its sequence
+  const int rounds = (ents + kFThreads - 1) / kFThreads;
+  for (int j = 0; j < rounds; ++j) {
+    const int e = j * kFThreads + t;
+    bool want = false;
+    if (e < ents) {
+      const int b = last_at_most(s_off, 0, a.B - 1, e), at = s_lo[b] + e - s_off[b];
+      const int id = a.table_in[(size_t)b * a.max_pages + at];
+      s_ent[e] = id;
+      want = id == -1 && at >= s_first[b];
+      if (!want && (id < 0 || id >= a.num_pages)) {
+        s_first[b] = 0x7fffffff;                           // every thread that writes it writes this
+        s_bad = 1;
+        if (lead) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
+      }
     }
+    const unsigned m = __ballot_sync(0xffffffffu, want);
+    if (lane == 0 && e < ents) s_mask[e >> 5] = m;
   }
   __syncthreads();
-  // 3. rank of every entry that needs a page, then the page
-  long long need = 0, all_n;
-  for (int j = 0; j < per; ++j) {
-    const int e = t * per + j;
-    if (e >= ents) break;
-    const int b = last_at_most(s_off, a.B, e);
-    if (s_ent[e] == -1 && s_lo[b] + e - s_off[b] >= s_first[b]) ++need;
+  if (s_bad) {                                             // the skipped sequences' entries need none
+    for (int j = 0; j < rounds; ++j) {
+      const int e = j * kFThreads + t;
+      bool want = false;
+      if (e < ents) {
+        const int b = last_at_most(s_off, 0, a.B - 1, e);
+        want = s_ent[e] == -1 && s_lo[b] + e - s_off[b] >= s_first[b];
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, want);
+      if (lane == 0 && e < ents) s_mask[e >> 5] = m;
+    }
+    __syncthreads();
   }
-  long long rank = block_scan(need, ws, all_n) - need;
+  // 3. rank of every entry that needs a page, then the page
+  const int nw = (ents + 31) / 32;
+  static_assert(kFusedEntries / 32 <= kFThreads, "one word a thread");
+  const int mine = t < nw ? __popc(s_mask[t]) : 0;
+  long long all_n;
+  const long long before = block_scan(mine, ws, all_n) - mine;
+  if (t < nw) s_pre[t] = (int)before;
+  __syncthreads();
   const bool pool_ok = count >= 0 && count <= a.capacity && all_n <= count, ok = pool_ok && fits;
   if (ok) {
-    for (int j = 0; j < per; ++j) {
-      const int e = t * per + j;
-      if (e >= ents) break;
-      const int b = last_at_most(s_off, a.B, e);
-      if (s_ent[e] == -1 && s_lo[b] + e - s_off[b] >= s_first[b]) s_ent[e] = a.free_pages[count - 1 - rank++];
+    for (int e = t; e < ents; e += kFThreads) {
+      const unsigned m = s_mask[e >> 5];
+      if ((m >> lane) & 1u) s_ent[e] = a.free_pages[count - 1 - (s_pre[e >> 5] + __popc(m & ((1u << lane) - 1u)))];
     }
   }
   if (lead) {
@@ -393,10 +416,19 @@ __global__ void __launch_bounds__(kFThreads) fused_kernel(TablesArgs a, int entr
   }
   // ... and of the slots, two rows a thread
   bool bad = false;
-  for (long long r2 = 2LL * gt; r2 < a.max_rows; r2 += 2LL * gn) {
+  for (long long rw = 2LL * (gt - lane); rw < a.max_rows; rw += 2LL * gn) {
+    // the warp's 64 rows lie on sequences b0 .. b1, mostly one
+    int b = 0;
+    if (rw < total) {
+      const int b0 = last_at_most(s_start, 0, a.B - 1, (int)rw);
+      const int end = (int)min(rw + 63, (long long)total - 1);
+      const int b1 = s_start[b0 + 1] > end ? b0 : last_at_most(s_start, b0, a.B - 1, end);
+      b = b0 == b1 ? b0 : last_at_most(s_start, b0, b1, (int)min(rw + 2 * lane, (long long)end));
+    }
+    const long long r2 = rw + 2 * lane;
+    if (r2 >= a.max_rows) continue;
     long long slot[2] = {-1, -1};
     int pos[2] = {-1, -1};
-    int b = r2 < total ? last_at_most(s_start, a.B, (int)r2) : 0;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const long long r = r2 + u;
@@ -460,7 +492,7 @@ extern "C" tidar_status tidar_build_tables(const tidar_tables_desc* d, const int
   // CTAs of one launch would read what others have already written.
   const long long entries = a.max_rows / a.ps + 2LL * a.B;
   if (a.B <= kFusedBatch && entries <= kFusedEntries && a.table_in != a.table_out && a.free_count != a.count_out) {
-    const size_t smem = (5 * (size_t)a.B + 2 + (size_t)entries) * sizeof(int);
+    const size_t smem = (5 * (size_t)a.B + 2 + (size_t)entries + 2 * ((entries + 31) / 32)) * sizeof(int);
     cudaError_t e = cudaSuccess;
     if (smem > 48 * 1024) e = cudaFuncSetAttribute(fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return cuda_status(e);
