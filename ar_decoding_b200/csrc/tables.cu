@@ -351,22 +351,35 @@ __global__ void __launch_bounds__(kFThreads) fused_kernel(TablesArgs a, int entr
   __syncthreads();
   // 2. the entries in use, and which need a page; a bad one skips its sequence
   const int rounds = (ents + kFThreads - 1) / kFThreads;
-  for (int j = 0; j < rounds; ++j) {
-    const int e = j * kFThreads + t;
-    bool want = false;
-    if (e < ents) {
-      const int b = last_at_most(s_off, 0, a.B - 1, e), at = s_lo[b] + e - s_off[b];
-      const int id = a.table_in[(size_t)b * a.max_pages + at];
-      s_ent[e] = id;
-      want = id == -1 && at >= s_first[b];
-      if (!want && (id < 0 || id >= a.num_pages)) {
-        s_first[b] = 0x7fffffff;                           // every thread that writes it writes this
-        s_bad = 1;
-        if (lead) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
+  constexpr int kU = 4;                                    // rounds whose loads are in flight together
+  for (int j0 = 0; j0 < rounds; j0 += kU) {
+    int seq[kU], at[kU], id[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int e = (j0 + u) * kFThreads + t;
+      id[u] = 0;
+      if (e < ents) {
+        seq[u] = last_at_most(s_off, 0, a.B - 1, e);
+        at[u] = s_lo[seq[u]] + e - s_off[seq[u]];
+        id[u] = a.table_in[(size_t)seq[u] * a.max_pages + at[u]];
       }
     }
-    const unsigned m = __ballot_sync(0xffffffffu, want);
-    if (lane == 0 && e < ents) s_mask[e >> 5] = m;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int e = (j0 + u) * kFThreads + t;
+      bool want = false;
+      if (e < ents) {
+        s_ent[e] = id[u];
+        want = id[u] == -1 && at[u] >= s_first[seq[u]];
+        if (!want && (id[u] < 0 || id[u] >= a.num_pages)) {
+          s_first[seq[u]] = 0x7fffffff;                    // every thread that writes it writes this
+          s_bad = 1;
+          if (lead) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
+        }
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, want);
+      if (lane == 0 && e < ents) s_mask[e >> 5] = m;
+    }
   }
   __syncthreads();
   if (s_bad) {                                             // the skipped sequences' entries need none
@@ -392,6 +405,7 @@ __global__ void __launch_bounds__(kFThreads) fused_kernel(TablesArgs a, int entr
   __syncthreads();
   const bool pool_ok = count >= 0 && count <= a.capacity && all_n <= count, ok = pool_ok && fits;
   if (ok) {
+#pragma unroll 4
     for (int e = t; e < ents; e += kFThreads) {
       const unsigned m = s_mask[e >> 5];
       if ((m >> lane) & 1u) s_ent[e] = a.free_pages[count - 1 - (s_pre[e >> 5] + __popc(m & ((1u << lane) - 1u)))];
