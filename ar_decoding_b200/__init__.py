@@ -177,9 +177,7 @@ def lib():
         L.tidar_step_attn_kv4_plan.restype = ctypes.c_int
         L.tidar_commit_kv4.argtypes = [P, P, P, P, P, P]
         L.tidar_commit_kv4.restype = ctypes.c_int
-        L.tidar_linear_fused_workspace_bytes.argtypes = [I, I, I]
-        L.tidar_linear_fused_workspace_bytes.restype = S
-        L.tidar_linear_fused.argtypes = [I, I, I, ctypes.c_int, P, P, P, ctypes.c_int, P, P, P, S, P]
+        L.tidar_linear_fused.argtypes = [I, I, I, ctypes.c_int, P, P, P, ctypes.c_int, P, P, P]
         L.tidar_linear_fused.restype = ctypes.c_int
         _lib = L
     return _lib
@@ -1016,24 +1014,13 @@ def commit_kv4(cache, accept_count, k, *, head_dim, max_prefix_len, released=Non
     return released, num_released
 
 
-def linear_fused_workspace_bytes(rows: int, out_features: int, in_features: int) -> int:
-    return int(lib().tidar_linear_fused_workspace_bytes(int(rows), int(out_features), int(in_features)))
-
-
-@functools.lru_cache(maxsize=1024)
-def _linear_need(rows, N, K, device):
-    """Workspace bytes of these sizes on `device`, the current one."""
-    return linear_fused_workspace_bytes(rows, N, K)
-
-
-def linear_fused(x, w, *, bias=None, activation="none", residual=None, out=None, workspace=None, stream=None):
+def linear_fused(x, w, *, bias=None, activation="none", residual=None, out=None, stream=None):
     """y = activation(x w^T + bias) + residual (bf16; x [..., in], w [out][in])
     on the tensor cores, rounded once.  ``activation``: none, relu, gelu (erf),
     gelu_tanh or silu.  ``residual`` has y's shape and may be ``out`` itself."""
     if _away(x, "x", stream):
         with _on(x.device, stream):
-            return linear_fused(x, w, bias=bias, activation=activation, residual=residual, out=out,
-                                workspace=workspace)
+            return linear_fused(x, w, bias=bias, activation=activation, residual=residual, out=out)
     _dev(x, "x", torch.bfloat16)
     dev = x.device
     _dev(w, "w", torch.bfloat16, dev)
@@ -1053,15 +1040,9 @@ def linear_fused(x, w, *, bias=None, activation="none", residual=None, out=None,
         out = x.new_empty(shape)
     else:
         _shaped(out, "out", shape, torch.bfloat16, dev)
-    need = _linear_need(rows, N, K, dev.index)
-    if workspace is None and not need:
-        ws, wbytes = None, 0
-    else:
-        workspace, wbytes = _scratch(need, workspace, dev)
-        ws = workspace.data_ptr()
     st = lib().tidar_linear_fused(rows, N, K, BF16, x.data_ptr(), w.data_ptr(),
                                   None if bias is None else bias.data_ptr(), act,
-                                  None if residual is None else residual.data_ptr(), out.data_ptr(), ws, wbytes,
+                                  None if residual is None else residual.data_ptr(), out.data_ptr(),
                                   _raw_stream(dev.index))
     if st:
         _check(st, "tidar_linear_fused")

@@ -723,39 +723,25 @@ tidar_status tidar_linear(int32_t rows, int32_t out_features, int32_t in_feature
   return TIDAR_OK;
 }
 
-size_t tidar_linear_fused_workspace_bytes(int32_t rows, int32_t out_features, int32_t in_features) {
-  if (rows <= 0 || out_features <= 0 || in_features <= 0 || in_features % 8) return 0;
-  if (tidar::linear_pair_wanted(rows, in_features, out_features)) return 0;
-  const tidar::LinearPlan p = tidar::plan_linear_any(rows, in_features, out_features);
-  return p.ok ? p.ws_bytes : 0;
-}
-
 tidar_status tidar_linear_fused(int32_t rows, int32_t out_features, int32_t in_features, tidar_dtype dtype,
                                 const void* x, const void* w, const void* bias, tidar_activation activation,
-                                const void* residual, void* y, void* workspace, size_t workspace_bytes,
-                                tidar_stream_t stream) {
+                                const void* residual, void* y, tidar_stream_t stream) {
   if (rows < 0 || out_features <= 0 || in_features <= 0) return TIDAR_ERR_INVALID_ARG;
   if (activation < TIDAR_ACT_NONE || activation > TIDAR_ACT_SILU) return TIDAR_ERR_INVALID_ARG;
   if (dtype != TIDAR_BF16 || in_features % 8) return TIDAR_ERR_UNSUPPORTED;
   if (rows == 0) return TIDAR_OK;
   if (!x || !w || !y || !aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(bias) || !aligned16(residual))
     return TIDAR_ERR_INVALID_ARG;
-  const bool pair = tidar::linear_pair_wanted(rows, in_features, out_features);
-  if (!pair) {
-    const tidar::LinearPlan p = tidar::plan_linear_any(rows, in_features, out_features);
-    if (!p.ok) return TIDAR_ERR_UNSUPPORTED;
-    if (workspace_bytes < p.ws_bytes || (p.ws_bytes && !workspace) ||
-        (reinterpret_cast<uintptr_t>(workspace) & 255u))
-      return TIDAR_ERR_INVALID_ARG;
-  }
   tidar::LinearArgs a{};
-  a.T = rows; a.K = in_features; a.N = out_features; a.mode = 2;
-  a.x = x; a.w = w; a.y = y; a.ws = workspace;
+  a.T = rows; a.K = in_features; a.N = out_features;
+  a.x = x; a.w = w; a.y = y;
   a.bias = bias; a.residual = residual; a.act = activation;
   const tidar_status st = error_word(&a.err);
   if (st != TIDAR_OK) return st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = pair ? tidar::launch_linear_pair(a, s) : tidar::launch_linear(a, s);
+  const tidar::LinearSplitPlan p = tidar::plan_linear_split(rows, in_features, out_features);
+  const bool split = p.ok && p.cost <= tidar::linear_pair_cost(rows, in_features, out_features);
+  const cudaError_t e = split ? tidar::launch_linear_split(a, s) : tidar::launch_linear_pair(a, s);
   if (e == cudaErrorNotSupported) return TIDAR_ERR_UNSUPPORTED;
   return e == cudaSuccess ? TIDAR_OK : cuda_fail(e);
 }

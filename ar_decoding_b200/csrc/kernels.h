@@ -169,8 +169,7 @@ cudaError_t launch_reserve(const ReserveArgs& a, cudaStream_t s);
 
 // Projections on either side of the step attention (tcgen05 GEMM, weights
 // [N][K] bf16 as the A operand, token rows [T][K] bf16 as B).  mode 0: y
-// [T][N] bf16.  mode 2: y = act(x w^T + bias) + residual, any N, K a multiple
-// of 8.  mode 1: the query/key/value projection of the R rows of each
+// [T][N] bf16.  mode 1: the query/key/value projection of the R rows of each
 // sequence (T = B R, N = (Hq + 2 Hkv) 128), rotary embedding of queries and
 // keys at their zone positions, outputs q / k_blk / v_blk.
 struct LinearArgs {
@@ -184,9 +183,11 @@ struct LinearArgs {
   const int32_t* seq_lens;
   int Hq, Hkv, R, k, max_prefix;
   double log2_base;
-  const void* bias;      // mode 2: [N] bf16 or null
-  const void* residual;  // mode 2: [T][N] bf16 or null (may be y itself)
-  int act;               // mode 2: tidar_activation
+  // the fused epilogue's kernels: y = act(x w^T + bias) + residual, any N, K a
+  // multiple of 8
+  const void* bias;      // [N] bf16 or null
+  const void* residual;  // [T][N] bf16 or null (may be y itself)
+  int act;               // tidar_activation
   unsigned int* err;
   void* ws;          // plan.ws_bytes of device scratch (split partials), 256-byte aligned
 };
@@ -201,13 +202,19 @@ struct LinearPlan {
 // take (K not a multiple of 64, N not a multiple of 128).  The split count
 // depends on the current device's cluster occupancy (queried once).
 LinearPlan plan_linear(int T, int K, int N);
-// The same for any N and K: the last feature tile and the last 64-deep slice
-// of the reduction are partly outside the tensors, where TMA reads zeros.
-LinearPlan plan_linear_any(int T, int K, int N);
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
-// Mode 2 for many rows, on pairs of SMs (no workspace); wanted: the shapes for
-// which it is the faster kernel.
-bool linear_pair_wanted(int T, int K, int N);
+// The fused epilogue's two kernels (no workspace): pairs of SMs on 256 x 256 tiles
+// (many rows), and the reduction split over a cluster of pairs (few rows).  Their
+// costs are estimates in clocks; the cheaper one runs.
+struct LinearSplitPlan {
+  bool ok;
+  int tt, nt, n0, n1, ft, ks, stages;
+  uint32_t stage_bytes;
+  double cost;
+};
+LinearSplitPlan plan_linear_split(int T, int K, int N);
+cudaError_t launch_linear_split(const LinearArgs& a, cudaStream_t s);
+double linear_pair_cost(int T, int K, int N);
 cudaError_t launch_linear_pair(const LinearArgs& a, cudaStream_t s);
 
 }  // namespace tidar

@@ -30,6 +30,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "linear_act.cuh"
+#include "pair.cuh"
 #include "sm100.cuh"
 #include "tc05.cuh"
 
@@ -64,32 +65,6 @@ struct PairParams {
   int vec;            // N % 8 == 0: rows of y and residual are 16-byte aligned
   unsigned int* err;
 };
-
-// One copy of this CTA's half, counted on a barrier of either CTA of the pair.
-__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// Arrives on the barrier at the same offset in both CTAs once every MMA issued
-// so far is complete.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
-      : "memory");
-}
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
 
@@ -180,9 +155,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
           const uint64_t a = tc05::desc_k_sw128(sb + (uint32_t)s * kStage), b = tc05::desc_k_sw128(sb + (uint32_t)s * kStage + kHalf);
 #pragma unroll
           for (int kc = 0; kc < 4; ++kc) mma_pair(d, a + (uint64_t)(kc * 2), b + (uint64_t)(kc * 2), kIdesc, (k > 0 || kc > 0) ? 1u : 0u);
-          commit_pair(bar(BAR_EMPTY + s));
+          commit_pair(bar(BAR_EMPTY + s), (uint16_t)3);
         }
-        if (ok) commit_pair(bar(BAR_ACC + buf));
+        if (ok) commit_pair(bar(BAR_ACC + buf), (uint16_t)3);
       }
     }
     __syncwarp();
@@ -289,10 +264,13 @@ int resident_pairs() {
 
 }  // namespace
 
-bool linear_pair_wanted(int T, int K, int N) {
+// Clocks that the product takes here: waves of tiles times (their slices at 512
+// clocks of MMA) + filling the pipeline and the last tile's epilogue.
+double linear_pair_cost(int T, int K, int N) {
   const long long tiles = (long long)((T + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
-  (void)K;
-  return T > 288 && tiles >= 48 && tiles <= 0x3fffffffLL && resident_pairs() > 0;
+  const int r = resident_pairs();
+  if (r <= 0 || tiles > 0x3fffffffLL) return 1e300;
+  return (double)((tiles + r - 1) / r) * ((K + 63) / 64) * 512.0 + 9000.0;
 }
 
 cudaError_t launch_linear_pair(const LinearArgs& a, cudaStream_t s) {

@@ -25,10 +25,6 @@
 //
 // Epilogues:
 //   plain   y [T][N] bf16.
-//   fused   y = act(x w^T + bias) + residual, bias and residual bf16, all of it
-//           in fp32 and rounded once.  Here N is any size and K a multiple of 8:
-//           the parts of the last tiles outside the tensors read as zeros (TMA)
-//           and are not written.
 //   qkv     features [0, Hq D) are queries, then Hkv D keys, then Hkv D values;
 //           queries and keys get the rotate-half rotary embedding at the zone
 //           position of their row (draft d_r at P + r - 1, slot s of block j
@@ -51,7 +47,6 @@
 
 #include "common.cuh"
 #include "kernels.h"
-#include "linear_act.cuh"
 #include "sm100.cuh"
 
 namespace tidar {
@@ -73,11 +68,7 @@ struct LinParams {
   int ksplit;         // cluster size along the reduction
   int kb_total;       // K / 64
   uint32_t stage_bytes;
-  int mode;           // 0 plain, 1 qkv + rotary embedding, 2 fused epilogue
-  int ftiles;         // feature tiles, ceil(N / 128)
-  const __nv_bfloat16* bias;
-  const __nv_bfloat16* residual;
-  int act;
+  int mode;           // 0 plain, 1 qkv + rotary embedding
   void* y;
   void* q;
   void* kb;
@@ -159,7 +150,7 @@ __device__ __forceinline__ long long zone_position(int k, int row, int P) {
 
 // (token tile, feature tile) group of a CTA, and the first float of split
 // `split`'s partials in the workspace.
-__device__ __forceinline__ int lin_group(const LinParams& prm, int tt, int ft) { return tt * prm.ftiles + ft; }
+__device__ __forceinline__ int lin_group(const LinParams& prm, int tt, int ft) { return tt * (prm.N / 128) + ft; }
 __device__ __forceinline__ size_t lin_part_offset(const LinParams& prm, int tt, int ft, int split) {
   return ((size_t)lin_group(prm, tt, ft) * prm.ksplit + split) * (size_t)prm.nt * 128;
 }
@@ -199,31 +190,6 @@ __device__ __forceinline__ void lin_reduce(const LinParams& prm, const float* pa
       }
       const int tg = t0 + t;
       __nv_bfloat16* dst;
-      if (prm.mode == 2) {
-        const int f0 = ft * 128 + 4 * lane;               // features f0 .. f0+3, those below N
-        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(prm.y) + (size_t)tg * prm.N + f0;
-        const __nv_bfloat16* res = prm.residual ? prm.residual + (size_t)tg * prm.N + f0 : nullptr;
-        if (prm.N % 4 == 0) {                              // rows 8-byte aligned: one access each
-          if (f0 >= prm.N) continue;
-          float r4[4] = {0.f, 0.f, 0.f, 0.f}, b4[4] = {0.f, 0.f, 0.f, 0.f};
-          if (prm.bias) load_vec<__nv_bfloat16, 4>(prm.bias + f0, b4);
-          if (res) load_vec<__nv_bfloat16, 4>(res, r4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[e] = lin_act(acc[e] + b4[e], prm.act) + r4[e];
-          uint2 u2;
-          u2.x = lin_bf16x2(acc[0], acc[1]);
-          u2.y = lin_bf16x2(acc[2], acc[3]);
-          *reinterpret_cast<uint2*>(y) = u2;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (f0 + e >= prm.N) continue;
-            const float v = acc[e] + (prm.bias ? __bfloat162float(prm.bias[f0 + e]) : 0.f);
-            y[e] = __float2bfloat16_rn(lin_act(v, prm.act) + (res ? __bfloat162float(res[e]) : 0.f));
-          }
-        }
-        continue;
-      }
       if (prm.mode == 0) {
         dst = static_cast<__nv_bfloat16*>(prm.y) + (size_t)tg * prm.N + ft * 128;
       } else {
@@ -515,13 +481,8 @@ extern "C" int tidar_lin_trace_clear() {
 #endif
 
 LinearPlan plan_linear(int T, int K, int N) {
-  if (K % 64 || N % 128) return LinearPlan{};
-  return plan_linear_any(T, K, N);
-}
-
-LinearPlan plan_linear_any(int T, int K, int N) {
   LinearPlan p{};
-  if (T <= 0 || K <= 0 || N <= 0) return p;
+  if (T <= 0 || K <= 0 || N <= 0 || K % 64 || N % 128) return p;
   const int pad16 = (T + 15) / 16 * 16;
   if (T <= kLinMaxTile) {
     p.nt = pad16 <= 256 ? pad16 : (T + 31) / 32 * 32;
@@ -541,8 +502,8 @@ LinearPlan plan_linear_any(int T, int K, int N) {
   // one 64-wide k-block (about 0.5 us with every SM streaming).  Without a
   // device (host-only planning) the occupancy is taken as one cluster per ks
   // SMs.
-  const int kb = (K + 63) / 64;
-  const long long base = (long long)((N + 127) / 128) * p.tiles;
+  const int kb = K / 64;
+  const long long base = (long long)(N / 128) * p.tiles;
   constexpr double kFixed = 10.0, kReduce = 1.5;
   double best = 1e300;
   int best_ks = 1;
@@ -562,22 +523,18 @@ LinearPlan plan_linear_any(int T, int K, int N) {
 }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
-  const LinearPlan p = a.mode == 2 ? plan_linear_any(a.T, a.K, a.N) : plan_linear(a.T, a.K, a.N);
-  if (!p.ok || a.K % 8) return cudaErrorNotSupported;
+  const LinearPlan p = plan_linear(a.T, a.K, a.N);
+  if (!p.ok) return cudaErrorNotSupported;
   if (p.ws_bytes && (!a.ws || (reinterpret_cast<uintptr_t>(a.ws) & 255u))) return cudaErrorInvalidValue;
   LinParams prm{};
   prm.T = a.T; prm.K = a.K; prm.N = a.N;
   prm.nt = p.nt; prm.nsub = p.nsub; prm.stages = p.stages; prm.ksplit = p.ksplit;
-  prm.kb_total = (a.K + 63) / 64; prm.stage_bytes = p.stage_bytes;
+  prm.kb_total = a.K / 64; prm.stage_bytes = p.stage_bytes;
   prm.mode = a.mode; prm.y = a.y; prm.q = a.q; prm.kb = a.k_blk; prm.vb = a.v_blk;
   prm.seq_lens = a.seq_lens; prm.Hq = a.Hq; prm.Hkv = a.Hkv; prm.R = a.R; prm.kdraft = a.k;
   prm.max_prefix = a.max_prefix; prm.log2_base = a.log2_base; prm.err = a.err;
-  prm.ftiles = (a.N + 127) / 128;
-  prm.bias = static_cast<const __nv_bfloat16*>(a.bias);
-  prm.residual = static_cast<const __nv_bfloat16*>(a.residual);
-  prm.act = a.act;
   if (p.ws_bytes) {
-    const size_t groups = (size_t)prm.ftiles * p.tiles;
+    const size_t groups = (size_t)(a.N / 128) * p.tiles;
     prm.part = static_cast<float*>(a.ws);
     prm.stat = reinterpret_cast<int*>(static_cast<char*>(a.ws) +
                                       (groups * p.ksplit * (size_t)p.nt * 128 * sizeof(float) + 255) / 256 * 256);
@@ -597,7 +554,7 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   }
   cudaError_t e = lin_smem_attr();
   if (e != cudaSuccess) return e;
-  const dim3 grid(prm.ftiles, p.ksplit, p.tiles), cluster(1, p.ksplit, 1);
+  const dim3 grid(a.N / 128, p.ksplit, p.tiles), cluster(1, p.ksplit, 1);
   return launch_clustered(linear_tc05_kernel, grid, cluster, kLinThreads, p.smem, s, tw, tx, prm);
 }
 

@@ -537,7 +537,9 @@ tidar_status tidar_build_tables(const tidar_tables_desc* desc, const int32_t* pa
  *   (TIDAR_PART_STEP_KEYS: the step keys, read from k_blk / v_blk as they are;
  *   TIDAR_PART_APPEND: the draft rows are quantised and stored); lse_out may be
  *   NULL with STEP_KEYS.  desc->dtype is that of q, k_blk, v_blk and out.
- *   Paths: AUTO or TIDAR_PATH_SIMT for every shape; workspace as
+ *   Paths: AUTO; SIMT for every shape; for bf16 and head_dim 128, any page size,
+ *   DEC (R * G <= 16) and TC05; PAIR is not offered.  A NaN among the values that a
+ *   row attends makes the row's outputs NaN.  workspace as
  *   tidar_step_attn's, sized by tidar_step_attn_kv4_workspace_bytes.
  *   TIDAR_ERR_UNSUPPORTED when batch * num_kv_heads > 65535.
  * tidar_commit_kv4: tidar_commit over such a cache (rejected rows are zeroed).
@@ -632,8 +634,7 @@ tidar_status tidar_linear(int32_t rows, int32_t out_features, int32_t in_feature
  * [out_features] are bf16 or NULL; residual may be y itself.  Any out_features;
  * in_features a multiple of 8 (else TIDAR_ERR_UNSUPPORTED).  GELU is 0.5 v (1 +
  * erf(v / sqrt 2)), GELU_TANH its tanh form, SILU v / (1 + exp(-v)).  Every
- * pointer 16-byte aligned; workspace as tidar_linear's, sized by
- * tidar_linear_fused_workspace_bytes. */
+ * pointer 16-byte aligned; no workspace. */
 typedef enum {
   TIDAR_ACT_NONE = 0,
   TIDAR_ACT_RELU = 1,
@@ -641,11 +642,10 @@ typedef enum {
   TIDAR_ACT_GELU_TANH = 3,
   TIDAR_ACT_SILU = 4
 } tidar_activation;
-size_t tidar_linear_fused_workspace_bytes(int32_t rows, int32_t out_features, int32_t in_features);
 tidar_status tidar_linear_fused(int32_t rows, int32_t out_features, int32_t in_features,
                                 tidar_dtype dtype, const void* x, const void* w, const void* bias,
                                 tidar_activation activation, const void* residual, void* y,
-                                void* workspace, size_t workspace_bytes, tidar_stream_t stream);
+                                tidar_stream_t stream);
 size_t tidar_qkv_rope_workspace_bytes(const tidar_step_desc* desc, int32_t d_model);
 tidar_status tidar_qkv_rope(const tidar_step_desc* desc, int32_t d_model, const void* x,
                             const void* w_qkv, const int32_t* seq_lens, float rope_base,

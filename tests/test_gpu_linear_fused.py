@@ -123,10 +123,9 @@ def test_two_streams_and_capture():
     for s in streams:
         s.wait_stream(torch.cuda.current_stream())
         got.append(tidar.linear_fused(x, w, bias=b, activation="silu", residual=r, stream=s))
-    ws = torch.empty(max(256, tidar.linear_fused_workspace_bytes(272, 2048, 4096)), dtype=torch.uint8, device="cuda")
     out, g = torch.zeros_like(want), torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        tidar.linear_fused(x, w, bias=b, activation="silu", residual=r, out=out, workspace=ws)
+        tidar.linear_fused(x, w, bias=b, activation="silu", residual=r, out=out)
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for y in got) and torch.equal(out, want)

@@ -107,19 +107,13 @@ def test_commit_kv4_refusals(L):
 
 
 def test_linear_fused_refusals(L):
-    def call(T=5, N=100, K=64, dt=tidar.BF16, x=FAKE, w=FAKE, b=None, act=0, r=None, y=FAKE, ws=None, wsb=0):
-        return L.tidar_linear_fused(T, N, K, dt, x, w, b, act, r, y, ws, wsb, None)
+    def call(T=5, N=100, K=64, dt=tidar.BF16, x=FAKE, w=FAKE, b=None, act=0, r=None, y=FAKE):
+        return L.tidar_linear_fused(T, N, K, dt, x, w, b, act, r, y, None)
     for kw in (dict(T=-1), dict(N=0), dict(K=0), dict(act=5), dict(act=-1), dict(x=None), dict(w=None), dict(y=None),
                dict(x=MISALIGNED), dict(b=MISALIGNED), dict(r=MISALIGNED), dict(y=MISALIGNED)):
         assert call(**kw) == tidar.ERR_INVALID_ARG, kw
     assert call(K=63) == tidar.ERR_UNSUPPORTED and call(dt=tidar.F32) == tidar.ERR_UNSUPPORTED
     assert call(T=0, x=None) == tidar.OK
-    need = L.tidar_linear_fused_workspace_bytes(77, 1000, 1544)
-    assert need % 256 == 0
-    if need:
-        assert call(77, 1000, 1544, ws=FAKE, wsb=need - 1) == tidar.ERR_INVALID_ARG
-        assert call(77, 1000, 1544, ws=FAKE + 16, wsb=need) == tidar.ERR_INVALID_ARG
-    assert L.tidar_linear_fused_workspace_bytes(5, 100, 63) == 0
 
 
 def test_binding_refuses_host_tensors():
