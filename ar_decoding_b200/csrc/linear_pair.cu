@@ -116,20 +116,22 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
     if (lane == 0) {
-      int it = 0;                  // slices issued
+      int it = 0, s = 0;           // slices issued, ring position
+      uint32_t phase = 1;          // 1: the first round's stages are free
       bool ok = true;
+      const uint32_t full0 = mapa(bar(BAR_FULL), 0);
       for (int tile = cluster; ok && tile < tiles; tile += clusters) {
         int rt, ft;
         tile_of(prm, tile, rt, ft);
         const int r0 = rt * kTile + (int)rank * 128, f0 = ft * kTile + (int)rank * 128;
         for (int k = 0; k < prm.kb; ++k, ++it) {
-          const int s = it % kStages;
-          if (it >= kStages) ok = wait_bar(bar(BAR_EMPTY + s), (uint32_t)((it / kStages - 1) & 1), abort_flag, prm.err);
+          ok = wait_bar(bar(BAR_EMPTY + s), phase, abort_flag, prm.err);
           if (!ok) break;
           if (rank == 0) mbar_expect_tx(bar(BAR_FULL + s), 2u * kStage);
-          const uint32_t full = mapa(bar(BAR_FULL + s), 0), dst = sb + (uint32_t)s * kStage;
+          const uint32_t full = full0 + 8u * s, dst = sb + (uint32_t)s * kStage;
           tma_load_pair(dst, &tm_x, k * 64, r0, full);
           tma_load_pair(dst + kHalf, &tm_w, k * 64, f0, full);
+          if (++s == kStages) s = 0, phase ^= 1u;
         }
       }
       // drain: the first CTA's barriers count the copies of both
@@ -139,23 +141,24 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0 && rank == 0) {
-      int it = 0, n = 0;           // slices consumed, tiles done
+      int s = 0, n = 0;            // ring position, tiles done
+      uint32_t phase = 0;
       bool ok = true;
+      const uint64_t a0 = tc05::desc_k_sw128(sb);
       for (int tile = cluster; ok && tile < tiles; tile += clusters, ++n) {
         const int buf = n & 1;
         if (n >= 2) ok = wait_bar(bar(BAR_FREE + buf), (uint32_t)((n / 2 - 1) & 1), abort_flag, prm.err);
         if (!ok) break;
         tc05::fence_after();
         const uint32_t d = tmem + (uint32_t)(buf * kTile);
-        for (int k = 0; k < prm.kb; ++k, ++it) {
-          const int s = it % kStages;
-          ok = wait_bar(bar(BAR_FULL + s), (uint32_t)((it / kStages) & 1), abort_flag, prm.err);
+        for (int k = 0; k < prm.kb; ++k) {
+          ok = wait_bar(bar(BAR_FULL + s), phase, abort_flag, prm.err);
           if (!ok) break;
           tc05::fence_after();
-          const uint64_t a = tc05::desc_k_sw128(sb + (uint32_t)s * kStage), b = tc05::desc_k_sw128(sb + (uint32_t)s * kStage + kHalf);
-#pragma unroll
-          for (int kc = 0; kc < 4; ++kc) mma_pair(d, a + (uint64_t)(kc * 2), b + (uint64_t)(kc * 2), kIdesc, (k > 0 || kc > 0) ? 1u : 0u);
+          const uint64_t a = a0 + (uint64_t)s * (kStage >> 4);
+          mma_pair_x4(d, a, a + (kHalf >> 4), kIdesc, (uint32_t)k);
           commit_pair(bar(BAR_EMPTY + s), (uint16_t)3);
+          if (++s == kStages) s = 0, phase ^= 1u;
         }
         if (ok) commit_pair(bar(BAR_ACC + buf), (uint16_t)3);
       }

@@ -115,16 +115,23 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
     if (lane == 0) {
       const int f0 = ft * 256 + half * 128;
       const uint32_t full0 = mapa(bar(BAR_FULL), lead);
-      int issued = 0;
-      for (int i = 0; i < nkb; ++i) {
-        const int s = i % prm.stages;
-        const uint32_t dst = sb + (uint32_t)s * prm.stage_bytes, full = full0 + 8u * s;
-        if (i >= prm.stages && !wait_bar(bar(BAR_EMPTY + s), (uint32_t)((i / prm.stages - 1) & 1), abort_flag, prm.err)) break;
-        if (half == 0) mbar_expect_tx(bar(BAR_FULL + s), 2u * prm.stage_bytes);
-        tma_load_pair(dst, &tm_w, (kb0 + i) * 64, f0, full);
-        tma_load_pair(dst + kABytes, &tm_x0, (kb0 + i) * 64, t0 + half * (prm.n0 / 2), full);
-        if (prm.n1) tma_load_pair(dst + kABytes + (uint32_t)prm.n0 * 64u, &tm_x1, (kb0 + i) * 64, t0 + prm.n0 + half * (prm.n1 / 2), full);
-        issued = i + 1;
+      // ring position and phase are carried, not divided out: this one thread's
+      // instructions are what a slice costs when few rows make its bytes few
+      const int x0 = t0 + half * (prm.n0 / 2), x1 = t0 + prm.n0 + half * (prm.n1 / 2);
+      const uint32_t off1 = kABytes + (uint32_t)prm.n0 * 64u, tx = 2u * prm.stage_bytes;
+      const bool two = prm.n1 > 0;
+      uint32_t dst = sb, off = 0, phase = 1;               // phase 1: the first round's stages are free
+      int s = 0, issued = 0;
+      for (int k = kb0 * 64; issued < nkb; k += 64) {
+        if (!wait_bar(bar(BAR_EMPTY) + off, phase, abort_flag, prm.err)) break;
+        if (half == 0) mbar_expect_tx(bar(BAR_FULL) + off, tx);
+        tma_load_pair(dst, &tm_w, k, f0, full0 + off);
+        tma_load_pair(dst + kABytes, &tm_x0, k, x0, full0 + off);
+        if (two) tma_load_pair(dst + off1, &tm_x1, k, x1, full0 + off);
+        ++issued;
+        dst += prm.stage_bytes;
+        off += 8;
+        if (++s == prm.stages) s = 0, dst = sb, off = 0, phase ^= 1u;
       }
       // drain: the first CTA's barriers count the copies of both
       if (half == 0 && *abort_flag)
@@ -139,22 +146,21 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
     if (lane == 0 && half == 0) {
       const uint16_t pair = (uint16_t)(3u << lead);
       const uint32_t id0 = idesc(prm.n0), id1 = idesc(prm.n1);
-      bool ok = true;
+      const bool two = prm.n1 > 0;
+      const uint64_t a0 = tc05::desc_k_sw128(sb), step = prm.stage_bytes >> 4, b_off = kABytes >> 4,
+                     c_off = (kABytes + (uint32_t)prm.n0 * 64u) >> 4;
+      uint64_t a = a0;
+      uint32_t off = 0, phase = 0;
+      int s = 0;
       for (int i = 0; i < nkb; ++i) {
-        const int s = i % prm.stages;
-        ok = wait_bar(bar(BAR_FULL + s), (uint32_t)((i / prm.stages) & 1), abort_flag, prm.err);
-        if (!ok) break;
+        if (!wait_bar(bar(BAR_FULL) + off, phase, abort_flag, prm.err)) break;
         tc05::fence_after();
-        const uint32_t a_addr = sb + (uint32_t)s * prm.stage_bytes;
-        const uint64_t a = tc05::desc_k_sw128(a_addr), b0 = tc05::desc_k_sw128(a_addr + kABytes),
-                       b1 = tc05::desc_k_sw128(a_addr + kABytes + (uint32_t)prm.n0 * 64u);
-#pragma unroll
-        for (int kc = 0; kc < 4; ++kc) {
-          const uint32_t acc = (i > 0 || kc > 0) ? 1u : 0u;
-          mma_pair(tmem, a + (uint64_t)(kc * 2), b0 + (uint64_t)(kc * 2), id0, acc);
-          if (prm.n1) mma_pair(tmem + (uint32_t)prm.n0, a + (uint64_t)(kc * 2), b1 + (uint64_t)(kc * 2), id1, acc);
-        }
-        commit_pair(bar(BAR_EMPTY + s), pair);
+        mma_pair_x4(tmem, a, a + b_off, id0, (uint32_t)i);
+        if (two) mma_pair_x4(tmem + (uint32_t)prm.n0, a, a + c_off, id1, (uint32_t)i);
+        commit_pair(bar(BAR_EMPTY) + off, pair);
+        a += step;
+        off += 8;
+        if (++s == prm.stages) s = 0, a = a0, off = 0, phase ^= 1u;
       }
       commit_pair(bar(BAR_DONE), pair);   // every MMA issued above is complete
     }

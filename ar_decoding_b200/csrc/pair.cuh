@@ -19,11 +19,17 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
 }
 // Issued by one thread of the pair's first CTA: A rows and B rows are halves in
 // the two shared memories (at the same offsets), D the same columns of both TMEMs.
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// A 64-deep slice: four MMAs (the K-major descriptors step by 32 bytes, 2 in their
+// address field) as one asm block, so that the issuing thread spends its
+// instructions on the MMAs.  The first accumulates when acc != 0.
+__device__ __forceinline__ void mma_pair_x4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %10, 0;\n\tsetp.eq.b32 q, %10, %10;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %5, %9, p;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %2, %6, %9, q;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %3, %7, %9, q;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %4, %8, %9, q;\n\t}"
+      ::"r"(d), "l"(a), "l"(a + 2), "l"(a + 4), "l"(a + 6), "l"(b), "l"(b + 2), "l"(b + 4), "l"(b + 6), "r"(idesc), "r"(acc)
       : "memory");
 }
 // Arrives on the barrier at the same offset in the CTAs of `mask` (cluster
