@@ -14,9 +14,10 @@
 // epilogue applied.  No workspace, no second launch, and the sums do not depend
 // on timing.
 //
-// Six warps: 0 TMA producer, 1 MMA issuer (the pair's first CTA)
-// and TMEM owner, 2..5 move the accumulator from TMEM (lane = feature, column =
-// row) to shared memory; all reduce.  Rows, features and the reduction may end
+// Twelve warps: 0 TMA producer, 1 MMA issuer (the pair's first CTA) and TMEM owner,
+// 2..5 move the accumulator from TMEM (lane = feature, column = row) to shared
+// memory; all twelve reduce, with 16 rows' peers in flight a warp (six warps with
+// four in flight took 7 us over 136 rows of two splits).  Rows, features and the reduction may end
 // anywhere (TMA reads zeros outside).
 //
 // Every wait is bounded (~1 s): on expiry the CTA records TIDAR_DEVERR_TIMEOUT,
@@ -38,7 +39,7 @@ namespace tidar {
 
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxStages = 12;
 constexpr int kMaxRows = 384;                           // rows of a tile (TMEM columns, shared memory)
@@ -64,8 +65,72 @@ struct SplitParams {
   unsigned int* err;
 };
 
+__device__ __forceinline__ float4 ld_shared_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t idesc(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((256u >> 4) << 24);
+}
+
+// Rows [lo, hi) of the tile at t0, features f0 .. f0+3 of this lane: the sum of up
+// to KS splits' partial sums (in split order) and the epilogue.  One warp per row,
+// the peers' values of 16 / KS rows in flight before the first is used.
+template <int KS>
+__device__ __forceinline__ void reduce_rows(const SplitParams& prm, uint32_t sb, int half, int f0, int t0, int lo, int hi,
+                                            int warp, int lane) {
+  constexpr int U = 16 / KS > 4 ? 4 : 16 / KS;
+  const bool vec = prm.N % 4 == 0;                         // rows 8-byte aligned: one access each
+  float b4[4] = {0.f, 0.f, 0.f, 0.f};
+  if (prm.bias) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (f0 + e < prm.N) b4[e] = __bfloat162float(prm.bias[f0 + e]);
+  }
+  uint32_t peer[KS];
+#pragma unroll
+  for (int q = 0; q < KS; ++q) peer[q] = mapa(sb + 16u * (uint32_t)lane, (uint32_t)(2 * min(q, prm.ks - 1) + half));
+  for (int tb = lo + warp; tb < hi; tb += kWarps * U) {
+    float4 v[U][KS];
+    uint2 res[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = tb + kWarps * u;
+      if (t < hi) {
+#pragma unroll
+        for (int q = 0; q < KS; ++q)
+          if (q < prm.ks) v[u][q] = KS == 1 ? ld_shared_f32x4(sb + 16u * (uint32_t)lane + 512u * (uint32_t)t)
+                                            : ld_cluster_f32x4(peer[q] + 512u * (uint32_t)t);
+        if (prm.residual && vec) res[u] = *reinterpret_cast<const uint2*>(prm.residual + (size_t)(t0 + t) * prm.N + f0);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = tb + kWarps * u;
+      if (t >= hi) break;
+      float o[4] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w};
+#pragma unroll
+      for (int q = 1; q < KS; ++q)
+        if (q < prm.ks) o[0] += v[u][q].x, o[1] += v[u][q].y, o[2] += v[u][q].z, o[3] += v[u][q].w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = lin_act(o[e] + b4[e], prm.act);
+      __nv_bfloat16* y = prm.y + (size_t)(t0 + t) * prm.N + f0;
+      if (vec) {
+        if (prm.residual) {
+          const float2 r0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&res[u].x));
+          const float2 r1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&res[u].y));
+          o[0] += r0.x; o[1] += r0.y; o[2] += r1.x; o[3] += r1.y;
+        }
+        *reinterpret_cast<uint2*>(y) = make_uint2(tc05::cvt_bf16x2(o[0], o[1]), tc05::cvt_bf16x2(o[2], o[3]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (f0 + e < prm.N)
+            y[e] = __float2bfloat16_rn(o[e] + (prm.residual ? __bfloat162float(prm.residual[(size_t)(t0 + t) * prm.N + f0 + e]) : 0.f));
+      }
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -165,7 +230,7 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
       commit_pair(bar(BAR_DONE), pair);   // every MMA issued above is complete
     }
     __syncwarp();
-  } else {
+  } else if (warp < 6) {
     // ---------------------------------------------------------------- TMEM -> shared memory
     pdl_wait();
     pdl_trigger();
@@ -183,6 +248,9 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
           if (c + e < nvalid) part[(c + e) * 128 + f] = __uint_as_float(r[e]);
       }
     }
+  } else {
+    pdl_wait();
+    pdl_trigger();
   }
   tc05::fence_before();
   __syncthreads();
@@ -190,11 +258,11 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
   cluster_sync_all();              // every CTA's partial sums and status are in place
 
   // ------------------------------------------------------------------ reduce + write
-  // CTA (split, half): rows [split per, + per) of the tile, 128 features; one warp
-  // per row, lane l features 4l .. 4l+3, four rows' loads in flight.
+  // CTA (split, half): rows [split per, + per) of the tile.
   const int ks = prm.ks, per = (nvalid + ks - 1) / ks;
   const int lo = split * per, hi = min(nvalid, lo + per);
   bool valid = true;
+#pragma unroll 4
   for (int r = 0; r < 2 * ks; ++r) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa(sb + ring + 8u * kNumBars + 8u, (uint32_t)r)) : "memory");
@@ -202,61 +270,10 @@ linear_split_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_const
   }
   const int f0 = ft * 256 + half * 128 + 4 * lane;
   if (valid && f0 < prm.N) {
-    const bool vec = prm.N % 4 == 0;                       // rows 8-byte aligned: one access each
-    float b4[4] = {0.f, 0.f, 0.f, 0.f};
-    if (prm.bias) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (f0 + e < prm.N) b4[e] = __bfloat162float(prm.bias[f0 + e]);
-    }
-    constexpr int U = 4;
-    for (int tb = lo + warp; tb < hi; tb += kWarps * U) {
-      float acc[U][4];
-      uint2 res[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = tb + kWarps * u;
-        acc[u][0] = acc[u][1] = acc[u][2] = acc[u][3] = 0.f;
-        if (t < hi && prm.residual && vec)
-          res[u] = *reinterpret_cast<const uint2*>(prm.residual + (size_t)(t0 + t) * prm.N + f0);
-      }
-      for (int q = 0; q < ks; ++q) {
-        const uint32_t peer = mapa(sb, (uint32_t)(2 * q + half));
-        float4 v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int t = tb + kWarps * u;
-          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (t < hi) v[u] = ld_cluster_f32x4(peer + 4u * (uint32_t)(t * 128 + 4 * lane));
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          acc[u][0] += v[u].x; acc[u][1] += v[u].y; acc[u][2] += v[u].z; acc[u][3] += v[u].w;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = tb + kWarps * u;
-        if (t >= hi) break;
-        __nv_bfloat16* y = prm.y + (size_t)(t0 + t) * prm.N + f0;
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = lin_act(acc[u][e] + b4[e], prm.act);
-        if (vec) {
-          if (prm.residual) {
-            const float2 r0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&res[u].x));
-            const float2 r1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&res[u].y));
-            v[0] += r0.x; v[1] += r0.y; v[2] += r1.x; v[3] += r1.y;
-          }
-          *reinterpret_cast<uint2*>(y) = make_uint2(tc05::cvt_bf16x2(v[0], v[1]), tc05::cvt_bf16x2(v[2], v[3]));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (f0 + e < prm.N)
-              y[e] = __float2bfloat16_rn(v[e] + (prm.residual ? __bfloat162float(prm.residual[(size_t)(t0 + t) * prm.N + f0 + e]) : 0.f));
-        }
-      }
-    }
+    if (ks == 1) reduce_rows<1>(prm, sb, half, f0, t0, lo, hi, warp, lane);
+    else if (ks == 2) reduce_rows<2>(prm, sb, half, f0, t0, lo, hi, warp, lane);
+    else if (ks <= 4) reduce_rows<4>(prm, sb, half, f0, t0, lo, hi, warp, lane);
+    else reduce_rows<8>(prm, sb, half, f0, t0, lo, hi, warp, lane);
   }
   tc05::fence_before();
   __syncthreads();
