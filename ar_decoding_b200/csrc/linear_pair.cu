@@ -12,9 +12,9 @@
 //
 // Persistent clusters of two CTAs, tiles in groups of eight row tiles (rows
 // fastest, so the weights of a feature tile are read from HBM once and its rows
-// stay in L2).  Six warps: 0 TMA producer (each CTA loads its own halves and
-// counts them on the first CTA's barrier), 1 MMA issuer and TMEM owner, 2..5
-// epilogue.  Two accumulators of 256 columns alternate, so the epilogue of a tile
+// stay in L2).  Ten warps: 0 TMA producer (each CTA loads its own halves and
+// counts them on the first CTA's barrier), 1 MMA issuer and TMEM owner, 2..9
+// epilogue (a lane quarter and half of the columns each).  Two accumulators of 256 columns alternate, so the epilogue of a tile
 // (a thread owns a row: 64 contiguous bytes a store group) runs under the MMAs of
 // the next.  Rows, features and the reduction may end anywhere: TMA reads zeros
 // outside, stores are guarded.
@@ -38,7 +38,7 @@ namespace tidar {
 
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;
 constexpr int kTile = 256;                              // rows and features of a pair's tile
 constexpr int kStages = 6;
 constexpr uint32_t kHalf = 128u * 128u;                 // 128 rows x 64 bf16
@@ -50,7 +50,11 @@ constexpr int BAR_ACC = 2 * kStages;                    // + buffer: accumulator
 constexpr int BAR_FREE = 2 * kStages + 2;               // + buffer: accumulator read (the first CTA's)
 constexpr int kNumBars = 2 * kStages + 4;
 constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;   // [0] TMEM base, [1] abort flag
-constexpr uint32_t kSmem = kOffMisc + 16;
+// rows that are not 16-byte aligned are written through shared memory: 32 x 32
+// values an epilogue warp, the rows one float apart in banks
+constexpr int kEpWarps = 8;
+constexpr uint32_t kOffTile = kOffMisc + 16;
+constexpr uint32_t kSmem = kOffTile + kEpWarps * 32 * 33 * 4;
 static_assert(kSmem <= 232448, "shared memory budget");
 constexpr int kRowGroup = 8;                            // row tiles that share a sweep over the features
 
@@ -95,7 +99,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), i >= BAR_FREE ? 8u : 1u);
+    for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), i >= BAR_FREE ? 16u : 1u);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     prefetch_tmap(&tm_x);
@@ -167,6 +171,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   } else {
     // ---------------------------------------------------------------- epilogue
     const int q4 = warp & 3;       // TMEM lane quarter
+    const int c0 = ((warp - 2) >> 2) * (kTile / 2), c1 = c0 + kTile / 2;    // and half of the columns
     int n = 0;
     for (int tile = cluster; tile < tiles; tile += clusters, ++n) {
       const int buf = n & 1;
@@ -178,19 +183,20 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       const uint32_t src = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(buf * kTile);
       const size_t at = (size_t)row * prm.N + f0;
 #pragma unroll 1
-      for (int c = 0; c < kTile; c += 32) {
+      for (int c = c0; c < c1; c += 32) {
         uint32_t acc[32];
         tc05::tmem_ld32(src + (uint32_t)c, acc);
         tc05::tmem_wait_ld();
-        if (c + 32 == kTile) {     // the accumulator has been read: the next tile may overwrite it
+        if (c + 32 == c1) {        // this half of the accumulator has been read: the next tile may overwrite it
           tc05::fence_before();
           __syncwarp();
           if (lane == 0) arrive_cluster(mapa(bar(BAR_FREE + buf), 0));
         }
-        if (row >= prm.T || f0 + c >= prm.N) continue;
-        __nv_bfloat16* dst = prm.y + at + c;
-        const __nv_bfloat16* res = prm.residual ? prm.residual + at + c : nullptr;
+        if (f0 + c >= prm.N) continue;                     // warp-uniform
         if (prm.vec && f0 + c + 32 <= prm.N) {
+          if (row >= prm.T) continue;
+          __nv_bfloat16* dst = prm.y + at + c;
+          const __nv_bfloat16* res = prm.residual ? prm.residual + at + c : nullptr;
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             float b8[8], r8[8], v[8];
@@ -204,11 +210,22 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                                                             tc05::cvt_bf16x2(v[4], v[5]), tc05::cvt_bf16x2(v[6], v[7]));
           }
         } else {
+          // a feature a lane, a row an instruction: 64 contiguous bytes each (a row
+          // a thread took 48 us for 1111 x 2049 x 200)
+          float* st = reinterpret_cast<float*>(smem + kOffTile) + (warp - 2) * (32 * 33);
+          __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            if (f0 + c + e < prm.N) {
-              const float v = __uint_as_float(acc[e]) + (prm.bias ? __bfloat162float(prm.bias[f0 + c + e]) : 0.f);
-              dst[e] = __float2bfloat16_rn(lin_act(v, prm.act) + (res ? __bfloat162float(res[e]) : 0.f));
+          for (int e = 0; e < 32; ++e) st[lane * 33 + e] = __uint_as_float(acc[e]);
+          __syncwarp();
+          const int f = f0 + c + lane, rows = min(32, prm.T - (row - lane));
+          if (f < prm.N) {
+            const float bias = prm.bias ? __bfloat162float(prm.bias[f]) : 0.f;
+            const size_t first = (size_t)(row - lane) * prm.N + f;
+#pragma unroll 4
+            for (int r = 0; r < rows; ++r) {
+              const size_t o = first + (size_t)r * prm.N;
+              const float v = lin_act(st[r * 33 + lane] + bias, prm.act);
+              prm.y[o] = __float2bfloat16_rn(v + (prm.residual ? __bfloat162float(prm.residual[o]) : 0.f));
             }
           }
         }
@@ -267,13 +284,15 @@ int resident_pairs() {
 
 }  // namespace
 
-// Clocks that the product takes here: waves of tiles times (their slices at 512
-// clocks of MMA) + filling the pipeline and the last tile's epilogue.
+// Clocks that the product takes here, fitted to measurements: waves of tiles times
+// their slices (590 clocks each while a few tiles run, 760 when the device is full
+// and L2 is shared) + launch, pipeline fill and the last tile's epilogue (longer for
+// rows that are not 16-byte aligned).
 double linear_pair_cost(int T, int K, int N) {
   const long long tiles = (long long)((T + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
   const int r = resident_pairs();
   if (r <= 0 || tiles > 0x3fffffffLL) return 1e300;
-  return (double)((tiles + r - 1) / r) * ((K + 63) / 64) * 512.0 + 9000.0;
+  return (double)((tiles + r - 1) / r) * ((K + 63) / 64) * (tiles >= 56 ? 760.0 : 590.0) + (N % 8 ? 30000.0 : 16000.0);
 }
 
 cudaError_t launch_linear_pair(const LinearArgs& a, cudaStream_t s) {

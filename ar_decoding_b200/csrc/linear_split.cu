@@ -331,30 +331,36 @@ int resident(int ks) {
 LinearSplitPlan plan_linear_split(int T, int K, int N) {
   LinearSplitPlan p{};
   if (T <= 0 || K <= 0 || N <= 0) return p;
-  // row tiles of equal size, a multiple of 32
-  p.tt = (T + kMaxRows - 1) / kMaxRows;
-  p.nt = ((T + p.tt - 1) / p.tt + 31) / 32 * 32;
+  p.ft = (N + 255) / 256;
+  const int kb = (K + 63) / 64, least = (T + kMaxRows - 1) / kMaxRows;
+  // Row tiles and splits by an estimate in clocks, fitted to measurements: waves of
+  // clusters times (the slices of one split at 250 + bytes / 90, a quarter more when
+  // the device is full and L2 is shared, + 6000 a CTA, + 55
+  // a row that it reduces, + 3000 a further split), and no less than the weights
+  // take from HBM.  More row tiles than needed read the weights again, from L2.
+  // 272 x 4096 x 4096, row tiles / splits: 1/1 34.0, 1/2 21.9, 1/3 19.3, 1/4 31.2
+  // (its clusters of eight take two waves), 2/1 26.1, 2/2 17.3, 2/3 27.4 us.
+  double best = 1e300;
+  for (int tt = least; tt <= least + 2 && tt <= T; ++tt) {
+    const int nt = ((T + tt - 1) / tt + 31) / 32 * 32;
+    const uint32_t bytes = kABytes + (uint32_t)nt * 64u;
+    const long long tiles = (long long)p.ft * tt;
+    for (int ks = 1; ks <= kMaxSplit && ks <= kb; ++ks) {
+      const int r = resident(ks);
+      if (r <= 0) continue;
+      const double waves = (double)((tiles + r - 1) / r);
+      const double slice = (250.0 + bytes / 90.0) * (tiles * ks >= 66 ? 1.25 : 1.0);
+      const double busy = waves * ((double)((kb + ks - 1) / ks) * slice + 6000.0 + 55.0 * nt / ks + 3000.0 * (ks - 1));
+      const double cost = std::max(busy, 5000.0 + (double)N * K * 2.0 / 3000.0);
+      if (cost < best - 1e-9) best = cost, p.ks = ks, p.tt = tt, p.nt = nt, p.stage_bytes = bytes;
+    }
+  }
   p.n0 = p.nt <= 256 ? p.nt : (p.nt / 2 + 31) / 32 * 32;
   p.n1 = p.nt - p.n0;
-  p.ft = (N + 255) / 256;
-  p.stage_bytes = kABytes + (uint32_t)p.nt * 64u;
-  p.stages = std::min<int>(kMaxStages, (int)((kSmemMax - kTail) / p.stage_bytes));
-  const int kb = (K + 63) / 64;
-  const long long tiles = (long long)p.ft * p.tt;
-  // Time of a split count, in clocks: waves of clusters times (the slices of one
-  // split, each the slower of its copies at 64 bytes a clock and its MMAs, + a
-  // fixed cost a CTA) + the exchange.
-  const double slice = std::max((double)p.stage_bytes / 40.0, 2.0 * p.nt);
-  double best = 1e300;
-  for (int ks = 1; ks <= kMaxSplit && ks <= kb; ++ks) {
-    const int r = resident(ks);
-    if (r <= 0) continue;
-    const double waves = (double)((tiles + r - 1) / r);
-    const double cost = waves * ((double)((kb + ks - 1) / ks) * slice + 5000.0) + (ks > 1 ? 1500.0 : 0.0);
-    if (cost < best - 1e-9) best = cost, p.ks = ks;
-  }
+  p.tt = p.nt ? (T + p.nt - 1) / p.nt : 0;               // rounding may leave the last tile empty
+  p.stages = p.stage_bytes ? std::min<int>(kMaxStages, (int)((kSmemMax - kTail) / p.stage_bytes)) : 0;
   p.cost = best;
-  p.ok = p.ks > 0 && tiles <= 65535;
+  p.ok = p.ks > 0 && (long long)p.ft * p.tt <= 65535;
   return p;
 }
 

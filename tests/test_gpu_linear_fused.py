@@ -78,8 +78,16 @@ def test_neighbouring_memory_is_left_alone():
 
 
 def test_plain_epilogue_is_the_linear_layer():
+    # The two kernels cut the reduction at different places, and fp32 sums of the same
+    # products in another order differ in their last bits (a + b + c with a = -b =
+    # 2^24, c = 1 is 1 or 0), so their bf16 results need not be equal: both are within
+    # the tolerance of the same sum, and of each other within twice that.
     x, w, _, _ = data(9, 64, 256, 512)
-    assert torch.equal(tidar.linear_fused(x, w), tidar.linear(x, w))
+    want, tol = reference(x, w, None, "none", None)
+    a, b = tidar.linear_fused(x, w), tidar.linear(x, w)
+    check(a, want, tol)
+    check(b, want, tol)
+    check(a, b.double(), 2 * tol)
 
 
 def test_residual_in_place_and_leading_dims():
