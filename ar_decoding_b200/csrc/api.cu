@@ -48,6 +48,10 @@ tidar_status error_word(unsigned int** out) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + m && b < a + n;
+}
 
 }  // namespace
 
@@ -729,8 +733,17 @@ tidar_status tidar_linear_fused(int32_t rows, int32_t out_features, int32_t in_f
   if (rows < 0 || out_features <= 0 || in_features <= 0) return TIDAR_ERR_INVALID_ARG;
   if (activation < TIDAR_ACT_NONE || activation > TIDAR_ACT_SILU) return TIDAR_ERR_INVALID_ARG;
   if (dtype != TIDAR_BF16 || in_features % 8) return TIDAR_ERR_UNSUPPORTED;
+  constexpr int kMax = 1 << 30;                            // and 2^30 tiles of 256 x 256: 32-bit indices
+  if (rows > kMax || out_features > kMax || in_features > kMax ||
+      ((rows + 255LL) / 256) * ((out_features + 255LL) / 256) > kMax)
+    return TIDAR_ERR_UNSUPPORTED;
   if (rows == 0) return TIDAR_OK;
   if (!x || !w || !y || !aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(bias) || !aligned16(residual))
+    return TIDAR_ERR_INVALID_ARG;
+  // y is written while other tiles still read their operands
+  const size_t yb = 2 * (size_t)rows * out_features;
+  if (overlap(y, yb, x, 2 * (size_t)rows * in_features) || overlap(y, yb, w, 2 * (size_t)out_features * in_features) ||
+      overlap(y, yb, bias, 2 * (size_t)out_features) || (residual != y && overlap(y, yb, residual, yb)))
     return TIDAR_ERR_INVALID_ARG;
   tidar::LinearArgs a{};
   a.T = rows; a.K = in_features; a.N = out_features;

@@ -634,7 +634,9 @@ tidar_status tidar_linear(int32_t rows, int32_t out_features, int32_t in_feature
  * [out_features] are bf16 or NULL; residual may be y itself.  Any out_features;
  * in_features a multiple of 8 (else TIDAR_ERR_UNSUPPORTED).  GELU is 0.5 v (1 +
  * erf(v / sqrt 2)), GELU_TANH its tanh form, SILU v / (1 + exp(-v)).  Every
- * pointer 16-byte aligned; no workspace. */
+ * pointer 16-byte aligned; no workspace.  y may overlap nothing else that the
+ * call reads (TIDAR_ERR_INVALID_ARG); sizes above 2^30, or y above 2^30 tiles of
+ * 256 x 256, are TIDAR_ERR_UNSUPPORTED. */
 typedef enum {
   TIDAR_ACT_NONE = 0,
   TIDAR_ACT_RELU = 1,

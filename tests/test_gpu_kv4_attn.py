@@ -275,3 +275,16 @@ def test_captured_replayed_and_on_another_stream():
         assert torch.equal(first, want[0]) and torch.equal(other[0], want[0])
         assert not torch.equal(out, first)
         compare(st, out, lse)
+
+
+def test_wait_timeout_is_reported_and_recovered():
+    # the dequantising warps fill no block, so the bounded waits run out; the next call is right
+    st = make(77, [300], 8, 2, 128, 2, 64, "bf16")
+    tidar.debug_set(tidar.DEBUG_STARVE_ATTENTION_LOADS, 1)
+    try:
+        tidar.step_attn_kv4(st["q"], st["k_blk"], st["v_blk"], st["cache"], 2, max_prefix_len=300, path="tc05")
+    finally:
+        tidar.debug_set(tidar.DEBUG_STARVE_ATTENTION_LOADS, 0)
+    status, bits = tidar.device_status()
+    assert status == tidar.ERR_TIMEOUT and bits & tidar.DEVERR_TIMEOUT
+    compare(st, *run(st, path="tc05"))

@@ -116,6 +116,17 @@ def test_linear_fused_refusals(L):
     assert call(T=0, x=None) == tidar.OK
 
 
+def test_linear_fused_refuses_overlap_and_sizes_past_its_indices(L):
+    x, w, b, r, y = (FAKE + (i << 24) for i in range(5))           # 16 MB apart
+    def call(T=5, N=100, K=64, x=x, w=w, b=b, r=r, y=y):
+        return L.tidar_linear_fused(T, N, K, tidar.BF16, x, w, b, 0, r, y, None)
+    for kw in (dict(y=x), dict(y=w), dict(y=b), dict(y=r + 16), dict(y=r - 16), dict(y=x + 2 * 5 * 64 - 16),
+               dict(y=w - 2 * 5 * 100 + 8), dict(y=w + 16 * 100)):
+        assert call(**kw) == tidar.ERR_INVALID_ARG, kw
+    for kw in (dict(T=2**30 + 1), dict(N=2**30 + 1), dict(K=2**30 + 8), dict(T=2**30, N=2**20)):
+        assert call(**kw) == tidar.ERR_UNSUPPORTED, kw
+
+
 def test_binding_refuses_host_tensors():
     i32, f = torch.int32, torch.bfloat16
     table, lens = torch.full((2, 4), -1, dtype=i32), torch.ones(2, dtype=i32)
