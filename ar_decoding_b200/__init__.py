@@ -81,7 +81,8 @@ class Kv4Desc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("num_pages", ctypes.c_int32), ("dtype", ctypes.c_int32),
-                ("k_row_stride", ctypes.c_int64), ("v_row_stride", ctypes.c_int64)]
+                ("k_row_stride", ctypes.c_int64), ("v_row_stride", ctypes.c_int64),
+                ("zero_skipped", ctypes.c_int32)]
 
 
 class Sampling(ctypes.Structure):
@@ -774,10 +775,9 @@ def build_tables(page_table, ctx_lens, new_lens, pool, *, page_size, num_pages, 
     if max_rows < 0:
         raise ValueError(f"max_rows is {max_rows}")
     if not out:
-        # one allocation of the int32 results (positions first: 8-byte aligned)
-        pos, tab, cnt, sta = page_table.new_empty((max_rows + B * width + B + 2,)).split(
-            (max_rows, B * width, 1, B + 1))
-        tab = tab.view(B, width)
+        # one allocation of the smaller int32 results (positions first: 8-byte aligned)
+        tab = torch.empty_like(page_table)
+        pos, cnt, sta = torch.split_with_sizes(page_table.new_empty((max_rows + B + 2,)), (max_rows, 1, B + 1))
         slo = page_table.new_empty((max_rows,), dtype=torch.int64)
     else:
         new = page_table.new_empty
@@ -853,20 +853,24 @@ def _row_stride(t, name, dtype, dev):
     return t.stride(0) if T > 1 else H * D
 
 
-def _kv4_desc(cache, k, v, slots):
+def _kv4_desc(cache, k, v, slots, zero_skipped=0):
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("rows must be CUDA tensors [rows][Hkv][D]")
     dev = k.device
     T, H, D = k.shape
-    ks, vs = _row_stride(k, "k_rows", k.dtype, dev), _row_stride(v, "v_rows", k.dtype, dev)
-    if v.shape != k.shape:
-        raise ValueError(f"k_rows {tuple(k.shape)} and v_rows {tuple(v.shape)} disagree")
+    if (k.is_contiguous() and isinstance(v, torch.Tensor) and v.is_contiguous() and v.shape == k.shape and
+            v.dtype == k.dtype and v.device == dev):
+        ks = vs = 0
+    else:
+        ks, vs = _row_stride(k, "k_rows", k.dtype, dev), _row_stride(v, "v_rows", k.dtype, dev)
+        if v.shape != k.shape:
+            raise ValueError(f"k_rows {tuple(k.shape)} and v_rows {tuple(v.shape)} disagree")
     ps = _kv4_page_size(cache, D, dev)
     pages, heads = cache["k_pages"].shape[:2]
     if heads != H:
         raise ValueError(f"the cache holds {heads} heads, the rows {H}")
     _shaped(slots, "slots", (T,), torch.int64, dev)
-    return Kv4Desc(T, H, D, ps, pages, _dtype_code(k), ks, vs)
+    return Kv4Desc(T, H, D, ps, pages, _dtype_code(k), ks, vs, zero_skipped)
 
 
 def kv4_append(cache, k_rows, v_rows, slots, *, stream=None):
@@ -885,19 +889,22 @@ def kv4_append(cache, k_rows, v_rows, slots, *, stream=None):
 
 def kv4_gather(cache, slots, *, head_dim=None, dtype=torch.bfloat16, out=None, stream=None):
     """The values stored at ``slots`` [T]: (k_rows, v_rows) [T][Hkv][D].  Rows
-    whose slot is negative are left as they were (zeros when allocated here)."""
+    whose slot is negative or past the cache are left as they were in ``out``, and
+    zeros where the call allocates the rows."""
     if _away(slots, "slots", stream):
         with _on(slots.device, stream):
             return kv4_gather(cache, slots, head_dim=head_dim, dtype=dtype, out=out)
-    if out is None:
+    zeros = out is None
+    if zeros:
         if head_dim is None:
             raise ValueError("head_dim is needed when out is not given")
         if dtype not in (torch.float32, torch.bfloat16):
             raise ValueError(f"unsupported dtype {dtype}")
-        both = torch.zeros((2, slots.numel(), cache["k_pages"].shape[1], head_dim), dtype=dtype, device=slots.device)
-        out = (both[0], both[1])
-    k, v = out
-    d = _kv4_desc(cache, k, v, slots)
+        k = slots.new_empty((slots.numel(), cache["k_pages"].shape[1], head_dim), dtype=dtype)
+        v = torch.empty_like(k)
+    else:
+        k, v = out
+    d = _kv4_desc(cache, k, v, slots, zeros)
     if k.device != slots.device:
         raise ValueError(f"out is on {k.device}, the call's tensors are on {slots.device}")
     st = lib().tidar_kv4_gather(ctypes.byref(d), cache["k_pages"].data_ptr(), cache["v_pages"].data_ptr(),

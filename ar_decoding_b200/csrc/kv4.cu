@@ -20,6 +20,7 @@ constexpr int kQThreads = 256;
 
 struct Kv4RowsArgs {
   int rows, Hkv, ps;
+  int fill;                    // gather: zeros for rows without a slot
   uint32_t units;              // rows * 2 Hkv, below 2^31
   uint32_t div_mul, div_shift; // u / (2 Hkv) = (u div_mul >> 32) >> div_shift for u < 2^31
   long long nslots;            // num_pages * page_size
@@ -109,6 +110,13 @@ __global__ void __launch_bounds__(kQThreads) kv4_rows_kernel(Kv4RowsArgs a) {
         }
         store8<T>(p + 32 * G, x[G]);
       }
+    } else if (in && a.fill) {
+#pragma unroll
+      for (int G = 0; G < N; ++G) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[G][e] = 0.f;
+        store8<T>(p + 32 * G, x[G]);
+      }
     }
   }
   if (bad) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
@@ -151,7 +159,7 @@ tidar_status prepare(const tidar_kv4_desc* d, const void* k_pages, const void* v
   a.units = (uint32_t)d->rows * n;
   a.div_mul = (uint32_t)(((1ULL << (31 + l)) + n - 1) / n);
   a.div_shift = l - 1;
-  a.rows = d->rows; a.Hkv = d->num_kv_heads; a.ps = d->page_size;
+  a.rows = d->rows; a.Hkv = d->num_kv_heads; a.ps = d->page_size; a.fill = d->zero_skipped != 0;
   a.nslots = (long long)d->num_pages * d->page_size;
   a.k = const_cast<void*>(k); a.v = const_cast<void*>(v); a.slots = slots;
   a.k_pages = static_cast<uint8_t*>(const_cast<void*>(k_pages));

@@ -532,7 +532,8 @@ tidar_status tidar_build_tables(const tidar_tables_desc* desc, const int32_t* pa
  *   named twice is unspecified).  TIDAR_ERR_UNSUPPORTED when rows * 2 *
  *   num_kv_heads >= 2^31 (both calls).
  * tidar_kv4_gather: the values of the rows at `slots`, exact in either dtype;
- *   rows whose slot is negative or past the cache are left as they were.
+ *   rows whose slot is negative or past the cache (BAD_PAGE) are left as they
+ *   were, or zeroed if desc->zero_skipped.
  * tidar_step_attn_kv4: tidar_step_attn_part over such a cache: flags as there
  *   (TIDAR_PART_STEP_KEYS: the step keys, read from k_blk / v_blk as they are;
  *   TIDAR_PART_APPEND: the draft rows are quantised and stored); lse_out may be
@@ -554,6 +555,7 @@ typedef struct {
   tidar_dtype dtype;     /* of the rows */
   int64_t k_row_stride;  /* elements between rows; 0: Hkv * D */
   int64_t v_row_stride;
+  int32_t zero_skipped;  /* gather: rows without a slot are written as zeros */
 } tidar_kv4_desc;
 
 size_t tidar_kv4_page_bytes(int32_t page_size, int32_t head_dim);   /* 0: unsupported */

@@ -177,3 +177,23 @@ def test_commit_zeroes_rejected_rows(k, ps, D, B):
     np.testing.assert_array_equal(c["seq_lens"].cpu().numpy(), P + acc)
     assert int(num) == len(rel) and released.cpu().numpy()[:len(rel)].tolist() == rel
     assert (released.cpu().numpy()[len(rel):] == -1).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_without_a_slot_are_zeros_where_the_call_allocates(D, dtype):
+    c = tidar.kv4_cache(4, 3, 16, D, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                        torch.zeros(1, dtype=torch.int32, device="cuda"))
+    rows = torch.randn(9, 3, D, device="cuda").to(dtype)
+    tidar.kv4_append(c, rows, rows, torch.arange(9, device="cuda"))
+    slots = torch.tensor([-1, 0, 5, -7, 8, -1], device="cuda")
+    dirty = [torch.full((6, 3, D), float("nan"), device="cuda", dtype=dtype) for _ in range(4)]
+    del dirty                                             # what the call is given to allocate
+    k, v = tidar.kv4_gather(c, slots, head_dim=D, dtype=dtype)
+    want = [torch.full_like(k, 3.0) for _ in range(2)]
+    tidar.kv4_gather(c, slots, out=tuple(want))
+    dead = slots < 0
+    for got, ref in ((k, want[0]), (v, want[1])):
+        assert (got[dead] == 0).all() and (ref[dead] == 3).all()
+        assert torch.equal(got[~dead], ref[~dead])
+    assert tidar.device_status() == (tidar.OK, 0)
