@@ -271,13 +271,16 @@ bool path_supported(const tidar_step_desc* d, int path, bool kv4) {
   return path == 1 || (path == 2 && tc05_supported(d, kv4)) || (path == 3 && dec_supported(d, kv4));
 }
 
-size_t step_workspace_bytes(const tidar_step_desc* d, bool kv4) {
-  if (check_desc(d) != TIDAR_OK) return 0;
-  const Plan p = make_plan(d, choose_path(d, kv4), kv4);
+size_t plan_workspace_bytes(const tidar_step_desc* d, const Plan& p) {
   if (p.nsplit <= 1 || p.cluster_merge) return 0;     // one split, or merged in the kernel
   const size_t rows = (size_t)d->batch * tidar::rows_per_seq(d->k) * d->num_q_heads;
   return align256((size_t)p.nsplit * rows * d->head_dim * sizeof(float)) +
          align256((size_t)p.nsplit * rows * sizeof(float));
+}
+
+size_t step_workspace_bytes(const tidar_step_desc* d, bool kv4) {
+  if (check_desc(d) != TIDAR_OK) return 0;
+  return plan_workspace_bytes(d, make_plan(d, choose_path(d, kv4), kv4));
 }
 
 tidar_status step_plan(const tidar_step_desc* d, bool kv4, int32_t* path, int32_t* splits, int32_t* merge) {
@@ -344,7 +347,7 @@ tidar_status step_attn_impl(const tidar_step_desc* d, const tidar_kv_cache* c, c
   if (!path_supported(d, pth, kv4)) return TIDAR_ERR_UNSUPPORTED;
   if (kv4 && (long long)d->batch * d->num_kv_heads > 65535) return TIDAR_ERR_UNSUPPORTED;   // the launch grid
   const Plan p = make_plan(d, pth, kv4);
-  const size_t need = step_workspace_bytes(d, kv4);
+  const size_t need = plan_workspace_bytes(d, p);
   if (workspace_bytes < need) return TIDAR_ERR_INVALID_ARG;
   if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
     return TIDAR_ERR_INVALID_ARG;
