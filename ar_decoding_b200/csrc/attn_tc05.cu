@@ -74,19 +74,17 @@ constexpr int BAR_VEMPTY = 20;   // + stage: V stage free again (its PV MMA is d
 constexpr int kNumBars = 23;
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = kOffQ + kTileBytes;
-// KV4: dequantising warps.  A block of one operand is 16 groups of 8 keys, two
-// or three of them a warp's; a turn converts a K and a V block, and the raw
-// copies run two turns ahead.
-constexpr int kDqWarps = 7;
+// KV4: dequantising warps, 16 keys of every block each (the smallest page holds
+// them); a turn converts a K and a V block, and the raw copies run two turns ahead.
+constexpr int kDqWarp0 = 4, kDqWarps = 8;
 constexpr int kRawTurns = 2;
-constexpr int kRawPer = 3;
-constexpr uint32_t kRawGroup = 8 * 72;                  // codes, then scales
-constexpr uint32_t kRawTurn = 2 * kRawPer * kRawGroup;  // K groups, then V groups
+constexpr uint32_t kRawOp = 16 * 72;                    // codes, then scales
+constexpr uint32_t kRawTurn = 2 * kRawOp;               // K, then V
 // Warp roles and the shared-memory layout behind the rings.
 template <bool KV4> struct Tc {
-  static constexpr int kThreads = KV4 ? 768 : 576;
+  static constexpr int kThreads = KV4 ? 896 : 576;
   static constexpr int kMma = KV4 ? 0 : 1;              // MMA issuer and TMEM owner
-  static constexpr int kSoft0 = KV4 ? 1 + kDqWarps : 2; // first of the 16 softmax warps
+  static constexpr int kSoft0 = KV4 ? kDqWarp0 + kDqWarps : 2;   // first of the 16 softmax warps
   static constexpr int kRing = KV4 ? 2 : kStages;       // K and V ring depth
   static constexpr int kFull = KV4 ? kDqWarps : 1;      // arrivals that fill a stage
   static constexpr uint32_t kOffV = kOffK + kRing * kTileBytes;
@@ -167,21 +165,20 @@ __device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, boo
       "l"(src), "r"((int)on)
       : "memory");
 }
-// The dequantising warps (1 .. kDqWarps) of a KV4 CTA: Q, then the blocks of
-// the K and V rings.  A group is 8 neighbouring keys of one operand; lane
+// The dequantising warps of a KV4 CTA: Q, then the blocks of the K and V rings.
+// Warp w takes keys 16w .. 16w+15 of every block, two groups of eight; lane
 // (kk, y), kk = (lane/8) + 4 (lane/4 % 2), y = lane % 4, copies and converts
-// chunk y of key kk: eight dims of each of the four groups of 32, 16 bytes of
-// bf16 each.  Eight lanes then hold keys k and k + 4, whose swizzled 16-byte
+// chunk y of key kk of each: eight dims of each of the four groups of 32, 16 bytes
+// of bf16 each.  Eight lanes then hold keys k and k + 4, whose swizzled 16-byte
 // units fall into different halves of the 128-byte row: stores without bank
-// conflicts.  Warp w takes groups (w + i) % 7, + 7, .. of block i.  What a warp spends on
-// control (page ids, addresses, waits) is of the order of its conversions, so a
-// turn takes a K and a V block together.
+// conflicts.  What a warp spends on control (page ids, addresses, waits) is of the
+// order of its conversions, so a turn takes a K and a V block together.
 __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensorMap& tm_q, const CUtensorMap& tm_ks,
                                            const CUtensorMap& tm_vs, uint8_t* smem, uint32_t sb, const BlockPlan& bp,
                                            const int32_t* table, int b, int g, int rho0, volatile int* abort_flag) {
   using L = Tc<true>;
   const AttnArgs& a = prm.a;
-  const int w = ((int)threadIdx.x >> 5) - 1, lane = (int)threadIdx.x & 31;
+  const int w = ((int)threadIdx.x >> 5) - kDqWarp0, lane = (int)threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return sb + L::kOffBar + 8u * i; };
   if (w == 0 && lane == 0) {
     mbar_expect_tx(bar(BAR_Q), 2u * 128u * (uint32_t)(prm.rho_per_tile * a.G));
@@ -196,58 +193,50 @@ __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensor
   const uint32_t stride32 = (uint32_t)page_stride;       // below 2^32: 65535 heads at most
   const uint32_t raw0 = L::kOffRaw + (uint32_t)w * (kRawTurns * kRawTurn);
   const uint32_t own = (uint32_t)(kk * 64 + y * 16);
+  const int first = bp.k0 + 16 * w;                       // this warp's first key of block 0
   bool bad = false;
-  // Table entry of group `lane` (16 of them) of prefix block i, -1 where there is
-  // no key; checked a turn later, when it has arrived.
-  auto load_entries = [&](int i) -> int {
-    const int key = bp.k0 + 128 * i + 8 * (lane & 15);
+  // Table entry of this warp's keys of prefix block i, -1 where there is no key;
+  // checked a turn later, when it has arrived.
+  auto load_entry = [&](int i) -> int {
+    const int key = first + 128 * i;
     return i < bp.npb && key < bp.kend ? table[key >> lps] : -1;
-  };
-  // Turn j converts K(j) and V(j - 1); this warp's groups of block i are q, q + 7,
-  // q + 14 (below 16), q = (w + i) % 7.  The copies of a turn (one commit group) go
-  // into raw slot j % 2: the codes a group an instruction, the scales of all six
-  // groups in one (lanes 4t .. 4t+3 those of group t).  e_k, e_v: the checked
-  // table entries of blocks j and j - 1; q_k, q_v their first groups.
-  const int st_grp = lane >> 2;                            // 0..2 K, 3..5 V, above: none
-  const bool st_v = st_grp >= 3;
-  const uint32_t st_dst = sb + raw0 + (uint32_t)st_grp * kRawGroup + 512u + 16u * (lane & 3);
-  const uint8_t* st_base = (st_v ? vbase : kbase) + (size_t)ps * 64 + 16 * (lane & 3);
-  const int st_q = kDqWarps * (st_v ? st_grp - 3 : st_grp);
-  auto copy_turn = [&](int j, int e_k, int e_v, int q_k, int q_v) {
-    const uint32_t slot = (uint32_t)(j & 1) * kRawTurn;
-#pragma unroll
-    for (int t = 0; t < 2 * kRawPer; ++t) {
-      const bool v = t >= kRawPer;
-      const int q = (v ? q_v : q_k) + kDqWarps * (v ? t - kRawPer : t);
-      const int pg = __shfl_sync(0xffffffffu, v ? e_v : e_k, q & 15);
-      const uint32_t row = (uint32_t)(bp.k0 + 128 * (v ? j - 1 : j) + 8 * q) & (uint32_t)(ps - 1);
-      const uint8_t* src = (v ? vbase : kbase) + (uint64_t)(uint32_t)pg * stride32 + (row * 64 + own);
-      cp_async16_if(sb + raw0 + slot + t * kRawGroup + 16u * lane, src, q < 16 && pg >= 0);
-    }
-    const int q = (st_v ? q_v : q_k) + st_q;
-    const int pk = __shfl_sync(0xffffffffu, e_k, q & 15), pv = __shfl_sync(0xffffffffu, e_v, q & 15);
-    const int pg = st_v ? pv : pk;
-    const uint32_t row = (uint32_t)(bp.k0 + 128 * (st_v ? j - 1 : j) + 8 * q) & (uint32_t)(ps - 1);
-    cp_async16_if(st_dst + slot, st_base + (uint64_t)(uint32_t)pg * stride32 + row * 8,
-                  lane < 8 * kRawPer && q < 16 && pg >= 0);
-    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto checked = [&](int e, int i) -> int {                // a page that does not exist: reported, not copied
     if (e >= 0 && e < a.num_pages) return e;
-    if (i < bp.npb && bp.k0 + 128 * i + 8 * (lane & 15) < bp.kend) bad = true;
+    if (i < bp.npb && first + 128 * i < bp.kend) bad = true;
     return -1;
   };
-  // Converts this warp's groups of block i from `raw` into the ring tile.
-  auto convert = [&](auto is_v, const uint8_t* raw, uint32_t tile, int i, int q0, uint32_t live) {
-    const int left = bp.kend - bp.k0 - 128 * i;             // keys of the block that exist
-    const bool whole = left >= 128 && (live & 0xffffu) == 0xffffu;
+  // Turn j converts K(j) and V(j - 1), pages e_k and e_v; its copies (one commit
+  // group) go into raw slot j % 2: the codes 512 bytes an instruction, the scales
+  // of both operands in one (lanes 0..7 K, 8..15 V).
+  const bool st_v = lane >= 8;
+  const uint32_t st_dst = sb + raw0 + (st_v ? kRawOp : 0u) + 1024u + 16u * (lane & 7);
+  const uint8_t* st_base = (st_v ? vbase : kbase) + (size_t)ps * 64 + 16 * (lane & 7);
+  auto copy_turn = [&](int j, int e_k, int e_v) {
+    const uint32_t slot = (uint32_t)(j & 1) * kRawTurn;
+    const uint32_t row_k = (uint32_t)(first + 128 * j) & (uint32_t)(ps - 1);
+    const uint32_t row_v = (uint32_t)(first + 128 * (j - 1)) & (uint32_t)(ps - 1);
+    const uint8_t* src_k = kbase + (uint64_t)(uint32_t)e_k * stride32 + (row_k * 64 + own);
+    const uint8_t* src_v = vbase + (uint64_t)(uint32_t)e_v * stride32 + (row_v * 64 + own);
+    const uint32_t dst = sb + raw0 + slot + 16u * lane;
+    cp_async16_if(dst, src_k, e_k >= 0);
+    cp_async16_if(dst + 512u, src_k + 512, e_k >= 0);
+    cp_async16_if(dst + kRawOp, src_v, e_v >= 0);
+    cp_async16_if(dst + kRawOp + 512u, src_v + 512, e_v >= 0);
+    const int e = st_v ? e_v : e_k;
+    cp_async16_if(st_dst + slot, st_base + (uint64_t)(uint32_t)e * stride32 + (st_v ? row_v : row_k) * 8, lane < 16 && e >= 0);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // Converts this warp's keys of block i from `raw` into the ring tile; page: whether
+  // they lie on a valid one.
+  const uint32_t unit = (uint32_t)((y ^ kk) << 4);         // the swizzled place of units 0..3 of the row; 4..7: ^ 64
+  auto convert = [&](auto is_v, const uint8_t* raw, uint32_t tile, int i, bool page) {
+    const int left = bp.kend - first - 128 * i;             // keys that exist
 #pragma unroll
-    for (int j = 0; j < kRawPer; ++j) {
-      const int q = q0 + kDqWarps * j, key = 8 * q + kk;
-      if (q >= 16) break;
-      uint4 c = *reinterpret_cast<const uint4*>(raw + j * kRawGroup + 16 * lane);
-      uint2 sc = *reinterpret_cast<const uint2*>(raw + j * kRawGroup + 512 + 8 * kk);
-      if (!whole && (key >= left || !((live >> q) & 1u))) c = make_uint4(0, 0, 0, 0), sc = make_uint2(0, 0);
+    for (int t = 0; t < 2; ++t) {
+      uint4 c = *reinterpret_cast<const uint4*>(raw + 512 * t + 16 * lane);
+      uint2 sc = *reinterpret_cast<const uint2*>(raw + 1024 + 64 * t + 8 * kk);
+      if (!page || 8 * t + kk >= left) c = make_uint4(0, 0, 0, 0), sc = make_uint2(0, 0);
       uint32_t words[4] = {c.x, c.y, c.z, c.w};
       if constexpr (decltype(is_v)::value) {
         const uint32_t raw4[4] = {c.x, c.y, c.z, c.w};
@@ -255,7 +244,7 @@ __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensor
       }
       const uint32_t sp[4] = {__byte_perm(sc.x, 0, 0x1010), __byte_perm(sc.x, 0, 0x3232),
                               __byte_perm(sc.y, 0, 0x1010), __byte_perm(sc.y, 0, 0x3232)};
-      uint8_t* row = smem + tile + key * 128;
+      uint8_t* row = smem + tile + (16 * w + 8 * t + kk) * 128;
 #pragma unroll
       for (int G = 0; G < 4; ++G) {
         uint32_t o[4];
@@ -264,21 +253,21 @@ __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensor
           const __nv_bfloat162 x = __hmul2(kv4_codes2(words[G], e), *reinterpret_cast<const __nv_bfloat162*>(&sp[G]));
           o[e] = *reinterpret_cast<const uint32_t*>(&x);
         }
-        *reinterpret_cast<uint4*>(row + (G >> 1) * kChunkBytes + (((4 * (G & 1) + y) ^ (key & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(row + (G >> 1) * kChunkBytes + (G & 1 ? unit ^ 64u : unit)) =
             make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   };
   // Waits for a free stage, fills it (a step-key window by TMA) and arrives.
-  auto fill = [&](auto is_v, int i, const uint8_t* raw, int q0, uint32_t live) -> bool {
+  auto fill = [&](auto is_v, int i, const uint8_t* raw, bool page) -> bool {
     constexpr bool v = decltype(is_v)::value;
     const int s = i & 1;
     const uint32_t full = bar((v ? BAR_VFULL : BAR_KFULL) + s), tile = (v ? L::kOffV : kOffK) + (uint32_t)s * kTileBytes;
     if (i >= 2 && !warp_wait_bar(bar((v ? BAR_VEMPTY : BAR_KEMPTY) + s), (uint32_t)((i / 2 - 1) & 1), abort_flag, a.err))
       return false;
     if (i < bp.npb) {
-      convert(is_v, raw, tile, i, q0, live);
+      convert(is_v, raw, tile, i, page);
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
     } else if (lane == 0) {
@@ -295,39 +284,32 @@ __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensor
     return true;
   };
   static_assert(L::kRing == 2 && kRawTurns == 2, "stage and raw slot of a turn: its parity");
-  // At the start of turn j: the checked entries of blocks j + 1 (e1) and j + 2
-  // (e2); which groups of blocks j - 1, j, j + 1 lie on a valid page (lv, lk, ln);
-  // the first group of block j (qk).
+  // At the start of turn j: the checked entries of blocks j - 1 (ev), j (ek),
+  // j + 1 (e1) and j + 2 (e2).
   bool ok = !prm.starve;
-  int e1 = -1, e2 = -1, qk = w;
-  uint32_t lv = 0, lk = 0, ln = 0;
-  auto step = [](int q, int by) -> int { q += by; return q >= kDqWarps ? q - kDqWarps : q; };
+  int ev = -1, ek = -1, e1 = -1, e2 = -1;
   if (ok) {
-    const int r0 = load_entries(0), r1 = load_entries(1), r2 = load_entries(2);
-    const int e0 = checked(r0, 0);
+    const int r0 = load_entry(0), r1 = load_entry(1), r2 = load_entry(2);
+    ek = checked(r0, 0);
     e1 = checked(r1, 1);
     e2 = checked(r2, 2);
-    copy_turn(0, e0, -1, qk, 0);
-    copy_turn(1, e1, e0, step(qk, 1), qk);
-    lk = __ballot_sync(0xffffffffu, e0 >= 0);
-    ln = __ballot_sync(0xffffffffu, e1 >= 0);
+    copy_turn(0, ek, -1);
+    copy_turn(1, e1, ek);
   }
   for (int j = 0; ok && j <= bp.nb; ++j) {
-    const int e3 = load_entries(j + 3);
+    const int e3 = load_entry(j + 3);
     asm volatile("cp.async.wait_group %0;" ::"n"(kRawTurns - 1) : "memory");
     __syncwarp();
     const uint8_t* raw = smem + raw0 + (uint32_t)(j & 1) * kRawTurn;
-    if (j < bp.nb) ok = fill(std::false_type{}, j, raw, qk, lk);
-    if (ok && j >= 1) ok = fill(std::true_type{}, j - 1, raw + kRawPer * kRawGroup, step(qk, kDqWarps - 1), lv);
+    if (j < bp.nb) ok = fill(std::false_type{}, j, raw, ek >= 0);
+    if (ok && j >= 1) ok = fill(std::true_type{}, j - 1, raw + kRawOp, ev >= 0);
     if (!ok) break;
     __syncwarp();                                          // every lane has read the raw slot: refill it
-    copy_turn(j + 2, e2, e1, step(qk, 2), step(qk, 1));
-    lv = lk;
-    lk = ln;
-    ln = __ballot_sync(0xffffffffu, e2 >= 0);
+    copy_turn(j + 2, e2, e1);
+    ev = ek;
+    ek = e1;
     e1 = e2;
     e2 = checked(e3, j + 3);
-    qk = step(qk, 1);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (bad) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
@@ -365,12 +347,15 @@ __device__ __forceinline__ void append_kv4(const AttnArgs& a, const int32_t* tab
 
 // ------------------------------------------------------------------ the kernel
 // 18 warps: two SMSPs host five of them, so a thread may hold at most
-// 16384 / (5 * 32) -> 96 registers.  KV4: 24 warps, six an SMSP, launched with 80
-// registers a thread; the two warpgroups of the MMA issuer and the dequantising
-// warps give registers up to the four softmax warpgroups for the main loop:
-// 256 * 48 + 512 * 96 = 768 * 80.
-constexpr int kRegsKv4 = 80, kRegsOther = 48, kRegsSoft = 96;
-static_assert(256 * kRegsOther + 512 * kRegsSoft <= 768 * kRegsKv4, "register split");
+// 16384 / (5 * 32) -> 96 registers.  KV4: 28 warps, seven an SMSP, launched with 72
+// registers a thread; the warpgroups of the MMA issuer (three of its warps idle)
+// and of the dequantising warps give registers up to the four softmax warpgroups
+// for the main loop.
+constexpr int kRegsKv4 = 72, kRegsOther = 40, kRegsSoft = 96;
+static_assert(32 * kDqWarp0 * kRegsOther + 32 * kDqWarps * kRegsOther + 512 * kRegsSoft <= Tc<true>::kThreads * kRegsKv4,
+              "register split");
+constexpr int kBarRegs = 13;                            // named barrier; 1..12 are the softmax warps'
+static_assert(kDqWarp0 % 4 == 0 && kDqWarps % 4 == 0, "whole warpgroups");
 template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <bool KV4>
@@ -536,8 +521,12 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_q, const CUtenso
     if constexpr (KV4) {
       regs_dec<kRegsOther>();
       if (warp == L::kMma) issue_mmas();
-      else dequantise(prm, tm_q, tm_ks, tm_vs, smem, sb, bp, table, b, g, rho0, abort_flag);
+      else if (warp >= kDqWarp0) dequantise(prm, tm_q, tm_ks, tm_vs, smem, sb, bp, table, b, g, rho0, abort_flag);
       __syncwarp();
+      // Only when every softmax warp has its share may these take theirs back: a
+      // warp that is done early (an idle one, few blocks) would leave a softmax
+      // warp waiting for registers that nobody gives up.
+      asm volatile("bar.sync %0, %1;" ::"n"(kBarRegs), "n"(kThreads) : "memory");
       regs_inc<kRegsKv4>();
     }
   } else if (!KV4 && warp == 0) {
@@ -661,7 +650,10 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_q, const CUtenso
     issue_mmas();
   } else {
     // ---------------------------------------------------------------- softmax
-    if constexpr (KV4) regs_inc<kRegsSoft>();
+    if constexpr (KV4) {
+      regs_inc<kRegsSoft>();
+      asm volatile("bar.arrive %0, %1;" ::"n"(kBarRegs), "n"(kThreads) : "memory");
+    }
     // Sixteen warps from kSoft0.  Set t (block parity) = (warp-kSoft0)/8 owns S_t and
     // O_t; within a set, half hf = ((warp-kSoft0)/4)&1 takes columns [64hf, 64hf+64) of the rows of
     // TMEM lane quarter warp%4.  One thread = one half row.  The two halves of a
@@ -869,7 +861,8 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_q, const CUtenso
     owrite = write;
     olse = lse;
     if constexpr (KV4) {
-      __syncwarp();
+      // the warps of a warpgroup meet between two changes of their registers
+      asm volatile("bar.sync %0, 512;" ::"n"(kBarRegs + 1) : "memory");
       regs_dec<kRegsKv4>();
     }
     if (warp == 4 && lane == 0) TIDAR_TRACE_AT(1538);
