@@ -351,8 +351,8 @@ __device__ __forceinline__ void append_kv4(const AttnArgs& a, const int32_t* tab
 // registers a thread; the warpgroups of the MMA issuer (three of its warps idle)
 // and of the dequantising warps give registers up to the four softmax warpgroups
 // for the main loop.
-constexpr int kRegsKv4 = 72, kRegsOther = 40, kRegsSoft = 96;
-static_assert(32 * kDqWarp0 * kRegsOther + 32 * kDqWarps * kRegsOther + 512 * kRegsSoft <= Tc<true>::kThreads * kRegsKv4,
+constexpr int kRegsKv4 = 72, kRegsMma = 40, kRegsDq = 40, kRegsSoft = 96;
+static_assert(32 * kDqWarp0 * kRegsMma + 32 * kDqWarps * kRegsDq + 512 * kRegsSoft <= Tc<true>::kThreads * kRegsKv4,
               "register split");
 constexpr int kBarRegs = 13;                            // named barrier; 1..12 are the softmax warps'
 static_assert(kDqWarp0 % 4 == 0 && kDqWarps % 4 == 0, "whole warpgroups");
@@ -466,7 +466,7 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_q, const CUtenso
       // address / 16 (below 2^14 here), so a tile at base + delta has the
       // descriptor of base plus delta / 16.  Q's eight are fixed; a stage's
       // K and V ones are its ring slot's base plus constants, formed ahead of
-      // the eight-MMA asm blocks.
+      // the eight-MMA asm blocks (KV4: four at a time, a quarter of the registers).
       uint64_t dq[8];
 #pragma unroll
       for (int kc = 0; kc < 8; ++kc) dq[kc] = desc_k_sw128(sb + kOffQ + (kc >> 2) * kChunkBytes + (kc & 3) * 32);
@@ -477,10 +477,15 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_q, const CUtenso
         TIDAR_TRACE_AT(256 + min(blk, 255));
         fence_after();
         const uint64_t kbase = dk0 + (uint64_t)((st * kTileBytes) >> 4);
-        uint64_t dk[8];
+        if constexpr (KV4) {
+          mma_ss_x4(tmem + col_s(t), dq[0], kbase, kIdescS, 0u);
+          mma_ss_x4(tmem + col_s(t), dq[4], kbase + (kChunkBytes >> 4), kIdescS, 1u);
+        } else {
+          uint64_t dk[8];
 #pragma unroll
-        for (int kc = 0; kc < 8; ++kc) dk[kc] = kbase + (uint64_t)(((kc >> 2) * kChunkBytes + (kc & 3) * 32) >> 4);
-        mma_ss_x8(tmem + col_s(t), dq, dk, kIdescS, 0u);
+          for (int kc = 0; kc < 8; ++kc) dk[kc] = kbase + (uint64_t)(((kc >> 2) * kChunkBytes + (kc & 3) * 32) >> 4);
+          mma_ss_x8(tmem + col_s(t), dq, dk, kIdescS, 0u);
+        }
         mma_commit(bar(BAR_SFULL + t));
         mma_commit(bar(BAR_KEMPTY + st));
         TIDAR_TRACE_AT(512 + min(blk, 255));
@@ -494,14 +499,19 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_q, const CUtenso
         if (!wait_bar(bar(BAR_PFULL + t), (uint32_t)(j & 1), abort_flag, a.err)) break;
         fence_after();
         const uint64_t vbase = dv0 + (uint64_t)((st * kTileBytes) >> 4);
-        uint32_t pa[8];
-        uint64_t dv[8];
+        if constexpr (KV4) {
+          mma_ts_x4(tmem + col_o(t), tmem + col_s(t) + p_col(0), vbase, kIdescPV, j > 0 ? 1u : 0u);
+          mma_ts_x4(tmem + col_o(t), tmem + col_s(t) + p_col(4), vbase + ((4 * 2048) >> 4), kIdescPV, 1u);
+        } else {
+          uint32_t pa[8];
+          uint64_t dv[8];
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          pa[kk] = tmem + col_s(t) + p_col(kk);
-          dv[kk] = vbase + (uint64_t)((kk * 2048) >> 4);
+          for (int kk = 0; kk < 8; ++kk) {
+            pa[kk] = tmem + col_s(t) + p_col(kk);
+            dv[kk] = vbase + (uint64_t)((kk * 2048) >> 4);
+          }
+          mma_ts_x8(tmem + col_o(t), pa, dv, kIdescPV, j > 0 ? 1u : 0u);
         }
-        mma_ts_x8(tmem + col_o(t), pa, dv, kIdescPV, j > 0 ? 1u : 0u);
         mma_commit(bar(BAR_PVDONE + t));
         mma_commit(bar(BAR_VEMPTY + st));
         TIDAR_TRACE_AT(768 + min(b2, 255));
@@ -519,9 +529,13 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_q, const CUtenso
   } else if (KV4 && warp < kSoft0) {
     // one instruction for whole warpgroups: registers down, the roles, up again
     if constexpr (KV4) {
-      regs_dec<kRegsOther>();
-      if (warp == L::kMma) issue_mmas();
-      else if (warp >= kDqWarp0) dequantise(prm, tm_q, tm_ks, tm_vs, smem, sb, bp, table, b, g, rho0, abort_flag);
+      if (warp >= kDqWarp0) {
+        regs_dec<kRegsDq>();
+        dequantise(prm, tm_q, tm_ks, tm_vs, smem, sb, bp, table, b, g, rho0, abort_flag);
+      } else {
+        regs_dec<kRegsMma>();
+        if (warp == L::kMma) issue_mmas();
+      }
       __syncwarp();
       // Only when every softmax warp has its share may these take theirs back: a
       // warp that is done early (an idle one, few blocks) would leave a softmax
