@@ -144,6 +144,13 @@ __device__ __forceinline__ bool trace_cta() { return blockIdx.x == 0 && blockIdx
 using namespace tc05;
 static_assert((128 * kStageStride + 256) * 4 <= Tc<true>::kRing * kTileBytes + Tc<true>::kRing * kTileBytes, "row staging fits the rings");
 
+#define TIDAR_RW8(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+// Waits for this thread's TMEM loads; uses of r cannot move before it.
+__device__ __forceinline__ void wait_ld32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : TIDAR_RW8(0), TIDAR_RW8(8), TIDAR_RW8(16), TIDAR_RW8(24)::"memory");
+}
+#undef TIDAR_RW8
+
 // 64 score columns: one TMEM load, or two of 32 columns where the launch's 80
 // registers a thread do not hold the wide one's operands (KV4).
 template <bool KV4>
@@ -764,16 +771,11 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_q, const CUtenso
       if (live) {
         const uint64_t sl2x2 = f2_make(sl2, sl2), nbx2 = f2_make(nbase, nbase);
         uint64_t ls2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
-        uint32_t x[64];
-        ld_half_row<KV4>(trow + scol, x);
-        tmem_wait_ld();
         uint32_t pk[32];
-        // The same loop for full and masked blocks (invisible keys hold -inf
-        // in S since pass 1, and 2^-inf = 0).  Compiled as two copies, the
-        // common full-block one is scheduled without register spills.
-        auto exps = [&]() {
+        // N pairs of scores from x to P from pk
+        auto exps = [&](const uint32_t* x, uint32_t* pk, auto n) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
+          for (int c = 0; c < decltype(n)::value; ++c) {
             float v0, v1;
             f2_split(f2_fma(f2_make(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sl2x2, nbx2), v0, v1);
             const float p0 = ex2(v0), p1 = ex2(v1);
@@ -781,8 +783,26 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_q, const CUtenso
             pk[c] = cvt_bf16x2(p0, p1);
           }
         };
-        if (full) exps();
-        else exps();
+        if constexpr (KV4) {
+          // two quarters: the second's load runs under the first's exponentials, and
+          // fewer scores are held at a time
+          uint32_t xa[32], xb[32];
+          tmem_ld32(trow + scol, xa);
+          wait_ld32(xa);
+          tmem_ld32(trow + scol + 32, xb);
+          exps(xa, pk, std::integral_constant<int, 16>{});
+          wait_ld32(xb);
+          exps(xb, pk + 16, std::integral_constant<int, 16>{});
+        } else {
+          uint32_t x[64];
+          tmem_ld64(trow + scol, x);
+          tmem_wait_ld();
+          // The same loop for full and masked blocks (invisible keys hold -inf
+          // in S since pass 1, and 2^-inf = 0).  Compiled as two copies, the
+          // common full-block one is scheduled without register spills.
+          if (full) exps(x, pk, std::integral_constant<int, 32>{});
+          else exps(x, pk, std::integral_constant<int, 32>{});
+        }
         tmem_st32(trow + scol, pk);
         float la, lb, lc, ld;
         f2_split(ls2[0], la, lb);
