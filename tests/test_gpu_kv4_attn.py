@@ -5,7 +5,7 @@ Tolerances.  bf16: every p is rounded once (2^-8 of itself at most) before it
 meets V, the sum l is not, so the output moves by at most 2^-8 sum p|v| / l; the
 result's own rounding adds 2^-8 |out|.  A score is a sum of D products in fp32
 whose partial sums reach at most 143/7 of sum |q||k| (codes enter the matrix
-product offset by 136): D/16 + 8 roundings of 2^-23 of that, which is the lse's
+product offset by 136 at most): D/16 + 8 roundings of 2^-23 of that, which is the lse's
 error, and times sum p|v| the output's.  fp32: D + 8 roundings of 2^-23 of
 sum |q||k|, and 2^-23 a step of sums over the keys.
 """
@@ -288,3 +288,27 @@ def test_wait_timeout_is_reported_and_recovered():
     status, bits = tidar.device_status()
     assert status == tidar.ERR_TIMEOUT and bits & tidar.DEVERR_TIMEOUT
     compare(st, *run(st, path="tc05"))
+
+
+@pytest.mark.parametrize("k", [0, 4])
+@pytest.mark.parametrize("magnitude", [2.0 ** 126 * (1 - 2.0 ** -8), 2.0 ** 100, 2.0 ** -100, 2.0 ** -120])
+def test_values_at_the_ends_of_the_range_are_exact(k, magnitude):
+    # one key: the output is its value row as it is, on every path
+    H, D, ps = 2, 128, 16
+    g = torch.Generator().manual_seed(3)
+    row = torch.randint(-7, 8, (1, H, D), generator=g).float() / 7
+    row[..., ::32] = 1.0                                  # every group's maximum
+    v = (row * magnitude).bfloat16().cuda()
+    cache = tidar.kv4_cache(2, H, ps, D, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                            torch.ones(1, dtype=torch.int32, device="cuda"))
+    tidar.kv4_append(cache, torch.zeros_like(v), v, torch.zeros(1, dtype=torch.int64, device="cuda"))
+    want = tidar.kv4_gather(cache, torch.zeros(1, dtype=torch.int64, device="cuda"), head_dim=D)[1]
+    ref = kv4_ref.unpack(kv4_ref.pack(v.double().cpu().numpy()[0, :, None], False), 1, D, False)[:, 0]
+    assert (want.double().cpu().numpy()[0] == ref).all() and (want != 0).any()
+    R = 1 if k == 0 else k + k * k
+    q = torch.randn(1, R, 2 * H, D, generator=g).bfloat16().cuda()
+    blk = torch.zeros(1, R, H, D, dtype=torch.bfloat16, device="cuda")
+    for path in paths(k, 2, D, "bf16"):
+        out, _ = tidar.step_attn_kv4(q, blk, blk, cache, k, max_prefix_len=1, step_keys=False, append=False, path=path)
+        assert torch.equal(out, want[0].repeat_interleave(2, 0).expand(1, R, 2 * H, D)), path
+    assert tidar.device_status() == (tidar.OK, 0)
