@@ -74,19 +74,18 @@ constexpr int BAR_VEMPTY = 20;   // + stage: V stage free again (its PV MMA is d
 constexpr int kNumBars = 23;
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = kOffQ + kTileBytes;
-// KV4: dequantising warps, 16 keys of every block each (the smallest page holds
-// them); a turn converts a K and a V block, and the raw copies run two turns ahead.
-constexpr int kDqWarp0 = 4, kDqWarps = 8;
+// KV4: dequantising warps, four for K and four for V, 32 keys of every block each;
+// the raw copies run two blocks ahead.
+constexpr int kDqWarp0 = 4, kDqWarps = 8, kDqPer = kDqWarps / 2;
 constexpr int kRawTurns = 2;
-constexpr uint32_t kRawOp = 16 * 72;                    // codes, then scales
-constexpr uint32_t kRawTurn = 2 * kRawOp;               // K, then V
+constexpr uint32_t kRawTurn = 32 * 72;                  // codes, then scales
 // Warp roles and the shared-memory layout behind the rings.
 template <bool KV4> struct Tc {
   static constexpr int kThreads = KV4 ? 896 : 576;
   static constexpr int kMma = KV4 ? 0 : 1;              // MMA issuer and TMEM owner
   static constexpr int kSoft0 = KV4 ? kDqWarp0 + kDqWarps : 2;   // first of the 16 softmax warps
   static constexpr int kRing = KV4 ? 2 : kStages;       // K and V ring depth
-  static constexpr int kFull = KV4 ? kDqWarps : 1;      // arrivals that fill a stage
+  static constexpr int kFull = KV4 ? kDqPer : 1;        // arrivals that fill a stage
   static constexpr uint32_t kOffV = kOffK + kRing * kTileBytes;
   static constexpr uint32_t kOffRaw = kOffV + kRing * kTileBytes;
   static constexpr uint32_t kOffBar = kOffRaw + (KV4 ? kDqWarps * kRawTurns * kRawTurn : 0);
@@ -172,86 +171,89 @@ __device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, boo
       "l"(src), "r"((int)on)
       : "memory");
 }
-// The dequantising warps of a KV4 CTA: Q, then the blocks of the K and V rings.
-// Warp w takes keys 16w .. 16w+15 of every block, two groups of eight; lane
-// (kk, y), kk = (lane/8) + 4 (lane/4 % 2), y = lane % 4, copies and converts
-// chunk y of key kk of each: eight dims of each of the four groups of 32, 16 bytes
-// of bf16 each.  Eight lanes then hold keys k and k + 4, whose swizzled 16-byte
-// units fall into different halves of the 128-byte row: stores without bank
-// conflicts.  What a warp spends on control (page ids, addresses, waits) is of the
-// order of its conversions, so a turn takes a K and a V block together.
-__device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensorMap& tm_q, const CUtensorMap& tm_ks,
-                                           const CUtensorMap& tm_vs, uint8_t* smem, uint32_t sb, const BlockPlan& bp,
-                                           const int32_t* table, int b, int g, int rho0, volatile int* abort_flag) {
+// The dequantising warps of a KV4 CTA: four for the K ring (the first also brings
+// Q), four for V.  Warp w of them takes keys 32w .. 32w+31 of every block, four
+// groups of eight; lane (kk, y), kk = (lane/8) + 4 (lane/4 % 2), y = lane % 4,
+// copies and converts chunk y of key kk of each: eight dims of each of the four
+// groups of 32, 16 bytes of bf16 each.  Eight lanes then hold keys k and k + 4,
+// whose swizzled 16-byte units fall into different halves of the 128-byte row:
+// stores without bank conflicts.
+template <bool kV>
+__device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensorMap& tm_q, const CUtensorMap& tm_s,
+                                           uint8_t* smem, uint32_t sb, const BlockPlan& bp, const int32_t* table, int b, int g,
+                                           int rho0, volatile int* abort_flag) {
   using L = Tc<true>;
   const AttnArgs& a = prm.a;
-  const int w = ((int)threadIdx.x >> 5) - kDqWarp0, lane = (int)threadIdx.x & 31;
+  const int dw = ((int)threadIdx.x >> 5) - kDqWarp0, w = dw - (kV ? kDqPer : 0), lane = (int)threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return sb + L::kOffBar + 8u * i; };
-  if (w == 0 && lane == 0) {
+  if (!kV && w == 0 && lane == 0) {
     mbar_expect_tx(bar(BAR_Q), 2u * 128u * (uint32_t)(prm.rho_per_tile * a.G));
     tma_load_4d(sb + kOffQ, &tm_q, 0, g * a.G, rho0, b, bar(BAR_Q));
     tma_load_4d(sb + kOffQ + kChunkBytes, &tm_q, 64, g * a.G, rho0, b, bar(BAR_Q));
   }
   const int ps = a.page_size, lps = 31 - __clz(ps);
-  const size_t page_bytes = kv4_page_bytes(ps, 128), page_stride = (size_t)a.Hkv * page_bytes;
-  const uint8_t* kbase = static_cast<const uint8_t*>(a.k_pages) + (size_t)g * page_bytes;
-  const uint8_t* vbase = static_cast<const uint8_t*>(a.v_pages) + (size_t)g * page_bytes;
+  const size_t page_bytes = kv4_page_bytes(ps, 128);
+  const uint32_t stride32 = (uint32_t)(a.Hkv * page_bytes);        // below 2^32: 65535 heads at most
+  const uint8_t* base = static_cast<const uint8_t*>(kV ? a.v_pages : a.k_pages) + (size_t)g * page_bytes;
   const int kk = ((lane >> 3) & 3) + 4 * ((lane >> 2) & 1), y = lane & 3;
-  const uint32_t stride32 = (uint32_t)page_stride;       // below 2^32: 65535 heads at most
-  const uint32_t raw0 = L::kOffRaw + (uint32_t)w * (kRawTurns * kRawTurn);
+  const uint32_t raw0 = L::kOffRaw + (uint32_t)dw * (kRawTurns * kRawTurn);
   const uint32_t own = (uint32_t)(kk * 64 + y * 16);
-  const int first = bp.k0 + 16 * w;                       // this warp's first key of block 0
+  const int first = bp.k0 + 32 * w;                       // this warp's first key of block 0
   bool bad = false;
-  // Table entry of this warp's keys of prefix block i, -1 where there is no key;
-  // checked a turn later, when it has arrived.
-  auto load_entry = [&](int i) -> int {
+  // Table entries of the halves (16 keys, the smallest page) of this warp's keys of
+  // prefix block i, -1 where there is no key; checked a turn later, when they have
+  // arrived.
+  struct Pages { int lo, hi; };
+  auto load_entry = [&](int key, int i) -> int { return i < bp.npb && key < bp.kend ? table[key >> lps] : -1; };
+  auto load_pages = [&](int i) -> Pages {
     const int key = first + 128 * i;
-    return i < bp.npb && key < bp.kend ? table[key >> lps] : -1;
+    return Pages{load_entry(key, i), load_entry(key + 16, i)};
   };
-  auto checked = [&](int e, int i) -> int {                // a page that does not exist: reported, not copied
+  auto check = [&](int e, int key, int i) -> int {         // a page that does not exist: reported, not copied
     if (e >= 0 && e < a.num_pages) return e;
-    if (i < bp.npb && first + 128 * i < bp.kend) bad = true;
+    if (i < bp.npb && key < bp.kend) bad = true;
     return -1;
   };
-  // Turn j converts K(j) and V(j - 1), pages e_k and e_v; its copies (one commit
-  // group) go into raw slot j % 2: the codes 512 bytes an instruction, the scales
-  // of both operands in one (lanes 0..7 K, 8..15 V).
-  const bool st_v = lane >= 8;
-  const uint32_t st_dst = sb + raw0 + (st_v ? kRawOp : 0u) + 1024u + 16u * (lane & 7);
-  const uint8_t* st_base = (st_v ? vbase : kbase) + (size_t)ps * 64 + 16 * (lane & 7);
-  auto copy_turn = [&](int j, int e_k, int e_v) {
-    const uint32_t slot = (uint32_t)(j & 1) * kRawTurn;
-    const uint32_t row_k = (uint32_t)(first + 128 * j) & (uint32_t)(ps - 1);
-    const uint32_t row_v = (uint32_t)(first + 128 * (j - 1)) & (uint32_t)(ps - 1);
-    const uint8_t* src_k = kbase + (uint64_t)(uint32_t)e_k * stride32 + (row_k * 64 + own);
-    const uint8_t* src_v = vbase + (uint64_t)(uint32_t)e_v * stride32 + (row_v * 64 + own);
-    const uint32_t dst = sb + raw0 + slot + 16u * lane;
-    cp_async16_if(dst, src_k, e_k >= 0);
-    cp_async16_if(dst + 512u, src_k + 512, e_k >= 0);
-    cp_async16_if(dst + kRawOp, src_v, e_v >= 0);
-    cp_async16_if(dst + kRawOp + 512u, src_v + 512, e_v >= 0);
-    const int e = st_v ? e_v : e_k;
-    cp_async16_if(st_dst + slot, st_base + (uint64_t)(uint32_t)e * stride32 + (st_v ? row_v : row_k) * 8, lane < 16 && e >= 0);
+  auto checked = [&](Pages e, int i) -> Pages {
+    const int key = first + 128 * i;
+    return Pages{check(e.lo, key, i), check(e.hi, key + 16, i)};
+  };
+  // The copies of block i (one commit group) go into raw slot i % 2: the codes 512
+  // bytes an instruction, the scales in one (lanes 0..7 and 8..15 a half each).
+  const uint32_t st_dst = sb + raw0 + 2048u + 16u * (lane & 15);
+  const uint32_t st_own = (uint32_t)ps * 64u + 16u * (lane & 7);
+  auto copy_block = [&](int i, Pages e) {
+    const uint32_t dst = sb + raw0 + (uint32_t)(i & 1) * kRawTurn + 16u * lane;
+    const uint32_t row_lo = (uint32_t)(first + 128 * i) & (uint32_t)(ps - 1), row_hi = (row_lo + 16u) & (uint32_t)(ps - 1);
+    const uint8_t* lo = base + (uint64_t)(uint32_t)e.lo * stride32 + (row_lo * 64 + own);
+    const uint8_t* hi = base + (uint64_t)(uint32_t)e.hi * stride32 + (row_hi * 64 + own);
+    cp_async16_if(dst, lo, e.lo >= 0);
+    cp_async16_if(dst + 512u, lo + 512, e.lo >= 0);
+    cp_async16_if(dst + 1024u, hi, e.hi >= 0);
+    cp_async16_if(dst + 1536u, hi + 512, e.hi >= 0);
+    const bool h = lane >= 8;
+    const int pg = h ? e.hi : e.lo;
+    cp_async16_if(st_dst + (uint32_t)(i & 1) * kRawTurn,
+                  base + (uint64_t)(uint32_t)pg * stride32 + (st_own + (h ? row_hi : row_lo) * 8), lane < 16 && pg >= 0);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // Converts this warp's keys of block i from `raw` into the ring tile; page: whether
-  // they lie on a valid one.
+  // Converts this warp's keys of block i from `raw` into the ring tile; e: their pages.
   const uint32_t unit = (uint32_t)((y ^ kk) << 4);         // the swizzled place of units 0..3 of the row; 4..7: ^ 64
-  auto convert = [&](auto is_v, const uint8_t* raw, uint32_t tile, int i, bool page) {
+  auto convert = [&](const uint8_t* raw, uint32_t tile, int i, Pages pg) {
     const int left = bp.kend - first - 128 * i;             // keys that exist
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < 4; ++t) {
       uint4 c = *reinterpret_cast<const uint4*>(raw + 512 * t + 16 * lane);
-      uint2 sc = *reinterpret_cast<const uint2*>(raw + 1024 + 64 * t + 8 * kk);
-      if (!page || 8 * t + kk >= left) c = make_uint4(0, 0, 0, 0), sc = make_uint2(0, 0);
+      uint2 sc = *reinterpret_cast<const uint2*>(raw + 2048 + 64 * t + 8 * kk);
+      if ((t < 2 ? pg.lo : pg.hi) < 0 || 8 * t + kk >= left) c = make_uint4(0, 0, 0, 0), sc = make_uint2(0, 0);
       uint32_t words[4] = {c.x, c.y, c.z, c.w};
-      if constexpr (decltype(is_v)::value) {
+      if constexpr (kV) {
         const uint32_t raw4[4] = {c.x, c.y, c.z, c.w};
         kv4_value_to_key<4>(raw4, words);
       }
       const uint32_t sp[4] = {__byte_perm(sc.x, 0, 0x1010), __byte_perm(sc.x, 0, 0x3232),
                               __byte_perm(sc.y, 0, 0x1010), __byte_perm(sc.y, 0, 0x3232)};
-      uint8_t* row = smem + tile + (16 * w + 8 * t + kk) * 128;
+      uint8_t* row = smem + tile + (32 * w + 8 * t + kk) * 128;
 #pragma unroll
       for (int G = 0; G < 4; ++G) {
         uint32_t o[4];
@@ -266,54 +268,43 @@ __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensor
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   };
-  // Waits for a free stage, fills it (a step-key window by TMA) and arrives.
-  auto fill = [&](auto is_v, int i, const uint8_t* raw, bool page) -> bool {
-    constexpr bool v = decltype(is_v)::value;
-    const int s = i & 1;
-    const uint32_t full = bar((v ? BAR_VFULL : BAR_KFULL) + s), tile = (v ? L::kOffV : kOffK) + (uint32_t)s * kTileBytes;
-    if (i >= 2 && !warp_wait_bar(bar((v ? BAR_VEMPTY : BAR_KEMPTY) + s), (uint32_t)((i / 2 - 1) & 1), abort_flag, a.err))
-      return false;
-    if (i < bp.npb) {
-      convert(is_v, raw, tile, i, page);
+  static_assert(L::kRing == 2 && kRawTurns == 2, "stage and raw slot of a block: its parity");
+  // At the start of turn j: the checked pages of blocks j (ek), j + 1 (e1) and j + 2 (e2).
+  bool ok = !prm.starve;
+  Pages ek{-1, -1}, e1{-1, -1}, e2{-1, -1};
+  if (ok) {
+    const Pages r0 = load_pages(0), r1 = load_pages(1), r2 = load_pages(2);
+    ek = checked(r0, 0);
+    e1 = checked(r1, 1);
+    e2 = checked(r2, 2);
+    copy_block(0, ek);
+    copy_block(1, e1);
+  }
+  for (int j = 0; ok && j < bp.nb; ++j) {
+    const Pages e3 = load_pages(j + 3);
+    const int s = j & 1;
+    const uint32_t full = bar((kV ? BAR_VFULL : BAR_KFULL) + s), tile = (kV ? L::kOffV : kOffK) + (uint32_t)s * kTileBytes;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRawTurns - 1) : "memory");
+    __syncwarp();
+    // a free stage: filled (a step-key window by TMA), then the arrival
+    if (j >= 2) ok = warp_wait_bar(bar((kV ? BAR_VEMPTY : BAR_KEMPTY) + s), (uint32_t)((j / 2 - 1) & 1), abort_flag, a.err);
+    if (!ok) break;
+    if (j < bp.npb) {
+      convert(smem + raw0 + (uint32_t)s * kRawTurn, tile, j, ek);
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
     } else if (lane == 0) {
       if (w == 0) {
-        const CUtensorMap* map = v ? &tm_vs : &tm_ks;
-        const int win = bp.wins[i - bp.npb];
+        const int win = bp.wins[j - bp.npb];
         mbar_expect_tx(full, kTileBytes);
-        tma_load_4d(sb + tile, map, 0, g, win * 128, b, full);
-        tma_load_4d(sb + tile + kChunkBytes, map, 64, g, win * 128, b, full);
+        tma_load_4d(sb + tile, &tm_s, 0, g, win * 128, b, full);
+        tma_load_4d(sb + tile + kChunkBytes, &tm_s, 64, g, win * 128, b, full);
       } else {
         mbar_arrive(full);
       }
     }
-    return true;
-  };
-  static_assert(L::kRing == 2 && kRawTurns == 2, "stage and raw slot of a turn: its parity");
-  // At the start of turn j: the checked entries of blocks j - 1 (ev), j (ek),
-  // j + 1 (e1) and j + 2 (e2).
-  bool ok = !prm.starve;
-  int ev = -1, ek = -1, e1 = -1, e2 = -1;
-  if (ok) {
-    const int r0 = load_entry(0), r1 = load_entry(1), r2 = load_entry(2);
-    ek = checked(r0, 0);
-    e1 = checked(r1, 1);
-    e2 = checked(r2, 2);
-    copy_turn(0, ek, -1);
-    copy_turn(1, e1, ek);
-  }
-  for (int j = 0; ok && j <= bp.nb; ++j) {
-    const int e3 = load_entry(j + 3);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRawTurns - 1) : "memory");
-    __syncwarp();
-    const uint8_t* raw = smem + raw0 + (uint32_t)(j & 1) * kRawTurn;
-    if (j < bp.nb) ok = fill(std::false_type{}, j, raw, ek >= 0);
-    if (ok && j >= 1) ok = fill(std::true_type{}, j - 1, raw + kRawOp, ev >= 0);
-    if (!ok) break;
     __syncwarp();                                          // every lane has read the raw slot: refill it
-    copy_turn(j + 2, e2, e1);
-    ev = ek;
+    copy_block(j + 2, e2);
     ek = e1;
     e1 = e2;
     e2 = checked(e3, j + 3);
@@ -322,11 +313,9 @@ __device__ __forceinline__ void dequantise(const Tc05Params& prm, const CUtensor
   if (bad) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
   if (w == 0 && lane == 0 && *abort_flag) {
     // drain: no copy may still write shared memory when the CTA moves on
-    wait_quiet(bar(BAR_Q), 0);
-    for (int i = max(bp.npb, bp.nb - L::kRing); i < bp.nb; ++i) {
-      wait_quiet(bar(BAR_KFULL + i % L::kRing), (uint32_t)((i / L::kRing) & 1));
-      wait_quiet(bar(BAR_VFULL + i % L::kRing), (uint32_t)((i / L::kRing) & 1));
-    }
+    if (!kV) wait_quiet(bar(BAR_Q), 0);
+    for (int i = max(bp.npb, bp.nb - L::kRing); i < bp.nb; ++i)
+      wait_quiet(bar((kV ? BAR_VFULL : BAR_KFULL) + i % L::kRing), (uint32_t)((i / L::kRing) & 1));
   }
   __syncwarp();
 }
@@ -538,7 +527,8 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_q, const CUtenso
     if constexpr (KV4) {
       if (warp >= kDqWarp0) {
         regs_dec<kRegsDq>();
-        dequantise(prm, tm_q, tm_ks, tm_vs, smem, sb, bp, table, b, g, rho0, abort_flag);
+        if (warp < kDqWarp0 + kDqPer) dequantise<false>(prm, tm_q, tm_ks, smem, sb, bp, table, b, g, rho0, abort_flag);
+        else dequantise<true>(prm, tm_q, tm_vs, smem, sb, bp, table, b, g, rho0, abort_flag);
       } else {
         regs_dec<kRegsMma>();
         if (warp == L::kMma) issue_mmas();
