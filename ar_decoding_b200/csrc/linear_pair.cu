@@ -38,7 +38,8 @@ namespace tidar {
 
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kEpWarps = 16;
+constexpr int kThreads = 32 * (2 + kEpWarps);
 constexpr int kTile = 256;                              // rows and features of a pair's tile
 constexpr int kStages = 6;
 constexpr uint32_t kHalf = 128u * 128u;                 // 128 rows x 64 bf16
@@ -51,10 +52,9 @@ constexpr int BAR_FREE = 2 * kStages + 2;               // + buffer: accumulator
 constexpr int kNumBars = 2 * kStages + 4;
 constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;   // [0] TMEM base, [1] abort flag
 // rows that are not 16-byte aligned are written through shared memory: 32 x 32
-// values an epilogue warp, the rows one float apart in banks
-constexpr int kEpWarps = 8;
+// values an epilogue warp in two halves, the rows one float apart in banks
 constexpr uint32_t kOffTile = kOffMisc + 16;
-constexpr uint32_t kSmem = kOffTile + kEpWarps * 32 * 33 * 4;
+constexpr uint32_t kSmem = kOffTile + kEpWarps * 32 * 17 * 4;
 static_assert(kSmem <= 232448, "shared memory budget");
 constexpr int kRowGroup = 8;                            // row tiles that share a sweep over the features
 
@@ -99,7 +99,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), i >= BAR_FREE ? 16u : 1u);
+    for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), i >= BAR_FREE ? 2u * kEpWarps : 1u);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     prefetch_tmap(&tm_x);
@@ -171,7 +171,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   } else {
     // ---------------------------------------------------------------- epilogue
     const int q4 = warp & 3;       // TMEM lane quarter
-    const int c0 = ((warp - 2) >> 2) * (kTile / 2), c1 = c0 + kTile / 2;    // and half of the columns
+    constexpr int kCols = kTile / (kEpWarps / 4);
+    const int c0 = ((warp - 2) >> 2) * kCols, c1 = c0 + kCols;     // and its share of the columns
     int n = 0;
     for (int tile = cluster; tile < tiles; tile += clusters, ++n) {
       const int buf = n & 1;
@@ -187,7 +188,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         uint32_t acc[32];
         tc05::tmem_ld32(src + (uint32_t)c, acc);
         tc05::tmem_wait_ld();
-        if (c + 32 == c1) {        // this half of the accumulator has been read: the next tile may overwrite it
+        if (c + 32 == c1) {        // this share of the accumulator has been read: the next tile may overwrite it
           tc05::fence_before();
           __syncwarp();
           if (lane == 0) arrive_cluster(mapa(bar(BAR_FREE + buf), 0));
@@ -210,22 +211,26 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                                                             tc05::cvt_bf16x2(v[4], v[5]), tc05::cvt_bf16x2(v[6], v[7]));
           }
         } else {
-          // a feature a lane, a row an instruction: 64 contiguous bytes each (a row
-          // a thread took 48 us for 1111 x 2049 x 200)
-          float* st = reinterpret_cast<float*>(smem + kOffTile) + (warp - 2) * (32 * 33);
-          __syncwarp();
+          // a feature a lane, two rows an instruction: 32 contiguous bytes each (a
+          // row a thread took 48 us for 1111 x 2049 x 200)
+          float* st = reinterpret_cast<float*>(smem + kOffTile) + (warp - 2) * (32 * 17);
+          const int rows = min(32, prm.T - (row - lane));
 #pragma unroll
-          for (int e = 0; e < 32; ++e) st[lane * 33 + e] = __uint_as_float(acc[e]);
-          __syncwarp();
-          const int f = f0 + c + lane, rows = min(32, prm.T - (row - lane));
-          if (f < prm.N) {
-            const float bias = prm.bias ? __bfloat162float(prm.bias[f]) : 0.f;
-            const size_t first = (size_t)(row - lane) * prm.N + f;
+          for (int h = 0; h < 2; ++h) {
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) st[lane * 17 + e] = __uint_as_float(acc[16 * h + e]);
+            __syncwarp();
+            const int f = f0 + c + 16 * h + (lane & 15);
+            if (f < prm.N) {
+              const float bias = prm.bias ? __bfloat162float(prm.bias[f]) : 0.f;
+              const size_t first = (size_t)(row - lane) * prm.N + f;
 #pragma unroll 4
-            for (int r = 0; r < rows; ++r) {
-              const size_t o = first + (size_t)r * prm.N;
-              const float v = lin_act(st[r * 33 + lane] + bias, prm.act);
-              prm.y[o] = __float2bfloat16_rn(v + (prm.residual ? __bfloat162float(prm.residual[o]) : 0.f));
+              for (int r = lane >> 4; r < rows; r += 2) {
+                const size_t o = first + (size_t)r * prm.N;
+                const float v = lin_act(st[r * 17 + (lane & 15)] + bias, prm.act);
+                prm.y[o] = __float2bfloat16_rn(v + (prm.residual ? __bfloat162float(prm.residual[o]) : 0.f));
+              }
             }
           }
         }
