@@ -36,13 +36,25 @@
 // merge in this kernel (cluster_merge: each CTA stages its normalised rows in
 // shared memory and owners read their peers' rows over distributed shared
 // memory), or write fp32 partials to the workspace for a finalize launch.
-// KV4 (the 4-bit cache of kv4.cuh, any page size): 24 warps.  Warp 0 is the MMA
-// issuer, warps 1..7 take the producer's place for prefix blocks: they copy
-// codes and scales in groups of 8 keys (asynchronous copies, two turns ahead),
-// turn them into the bf16 values they stand for (exact) and write those into the
-// K and V rings in the layout that TMA would have left, in the order K0, K1, V0,
-// K2, V1, ..; warps 8..23 are the softmax warps.  Step-key windows still come by
-// TMA.  Rings of two stages make room for the raw groups.
+// KV4 (the 4-bit cache of kv4.cuh, any page size): 28 warps.  Warp 0 is the MMA
+// issuer (1..3 idle: registers are dealt out to whole warpgroups); warps 4..7 (K)
+// and 8..11 (V) take the producer's place for prefix blocks: they copy codes and
+// scales of 32 keys each (asynchronous copies, two blocks ahead), turn them into the
+// bf16 values they stand for (exact) and write those into the rings in the layout
+// that TMA would have left; warps 12..27 are the softmax warps.  Step-key windows
+// still come by TMA.  Rings of two stages make room for the raw rows.
+// Bound there: the bytes are 3.6 times fewer, but every tile of 128 packed rows
+// converts its blocks again, beside 16 softmax warps that want the same issue
+// slots.  32 q / 8 kv heads, 8192 keys, k = 16: 69.3 us (0.53 PFLOP/s; 55.3 over the
+// bf16 cache; 57-63 without the conversions); 32 sequences of 512 to 16384 keys at
+// k = 8: 682 us (0.47 PFLOP/s; bf16 515, without the conversions 590).  Steps: seven
+// converting warps that take a K and a V block in turn, in 24 warps of 80 registers
+// 85 / 838 us; eight in 28 warps of 72 82 / 765; the issuing thread without spilled
+// descriptors 75 / 732; the second softmax pass in two quarters 74 / 727; warps of
+// one operand, half the waits and fences, 69 / 682.  Not kept: the tiles of a
+// sequence as a cluster that shares the conversions (distributed shared memory moves
+// tens of GB/s an SM: 130 / 1046 us with bulk copies, 245 with remote stores); fewer
+// instructions a code pair (one multiply-add for subtract and multiply: no change).
 // Every mbarrier wait is bounded: on expiry the CTA records TIDAR_DEVERR_TIMEOUT,
 // stops issuing, drains what it issued (bounded), frees TMEM and exits.
 #include <cuda.h>

@@ -24,7 +24,9 @@
 // slots_kernel: the whole device, one thread per pair of token rows (one
 // 16-byte store of two slots), the row's sequence found by bisection of the
 // starts, which sit in shared memory up to kStartsMax sequences.
-// Serving admission (32 prompts, 524288 slots): 14.3 us in two launches.
+// Measured: 32 prompts (results of 4.5 MB) 13.2 us in one launch (14.3 in two), a
+// step of 256 sequences 7.4 us; both are launch, dependent loads and one round of
+// stores, 0.3 TB/s at most.
 #include <cooperative_groups.h>
 
 #include <algorithm>
