@@ -59,7 +59,7 @@ __device__ unsigned long long g_commit_trace[8];
 // kFused: the accept counts are not read but computed here from the chunk
 // statistics of a greedy verification (`f`), whose outputs the owner of each
 // sequence also writes (tidar_verify_commit).
-template <bool kFused>
+template <bool kFused, bool kKv4>
 __global__ void __launch_bounds__(kCThreads) commit_cluster_kernel(CommitArgs a, int slots, int per, int npm,
                                                                     GreedyAcceptArgs f) {
   __shared__ int s_g[kFused ? kCWarps : 1][kFused ? 16 * 16 : 1];   // per-warp block guesses
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kCThreads) commit_cluster_kernel(CommitArgs a,
   const int t0 = spread ? rank * kCThreads + (int)threadIdx.x : (int)threadIdx.x;
   const int tstep = spread ? C * kCThreads : kCThreads;
   const size_t row_bytes = (size_t)a.D * a.elem_bytes;
-  if (a.kv4) {
+  if constexpr (kKv4) {
     // 4-bit pages: one thread per (row, K or V, head), its codes and scales
     const int units = 2 * a.Hkv;
     const size_t page_bytes = kv4_page_bytes(ps, a.D);
@@ -344,7 +344,7 @@ bool commit_batch_ok(int B, int k, int page_size) {
   return commit_smem((B + 7) / 8, commit_npm(n, page_size)) <= kCommitSmemMax;
 }
 
-template <bool kFused>
+template <bool kFused, bool kKv4>
 cudaError_t launch_commit_t(const CommitArgs& a, const GreedyAcceptArgs& f, cudaStream_t s) {
   static int limit_cache[64];
   static bool smem_set[64];
@@ -353,11 +353,11 @@ cudaError_t launch_commit_t(const CommitArgs& a, const GreedyAcceptArgs& f, cuda
   // them faster than a cluster barrier takes), up to the largest cluster: with
   // a small batch the CTAs share the zeroing, and a small cluster finds its
   // SMs free while the previous kernel's CTAs still hold most of the others.
-  const size_t row_bytes = a.kv4 ? (size_t)(kv4_code_bytes(a.D) + kv4_scale_bytes(a.D)) : (size_t)a.D * a.elem_bytes;
+  const size_t row_bytes = kKv4 ? (size_t)(kv4_code_bytes(a.D) + kv4_scale_bytes(a.D)) : (size_t)a.D * a.elem_bytes;
   const size_t scrub = (size_t)a.B * a.n * 2 * a.Hkv * row_bytes;
   const int C = scrub <= (32u << 10)
                     ? 1
-                    : (int)std::min<size_t>(cluster_limit(commit_cluster_kernel<kFused>, kCThreads, limit_cache),
+                    : (int)std::min<size_t>(cluster_limit(commit_cluster_kernel<kFused, kKv4>, kCThreads, limit_cache),
                                             (scrub + (16u << 10) - 1) >> 14);
   const int per = (a.B + C - 1) / C;
   const int npm = commit_npm(a.n, a.page_size);
@@ -366,17 +366,18 @@ cudaError_t launch_commit_t(const CommitArgs& a, const GreedyAcceptArgs& f, cuda
   int dev = 0;
   cudaGetDevice(&dev);
   if (smem > 48 * 1024 && dev >= 0 && dev < 64 && !smem_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(commit_cluster_kernel<kFused>,
+    cudaError_t e = cudaFuncSetAttribute(commit_cluster_kernel<kFused, kKv4>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kCommitSmemMax);
     if (e != cudaSuccess) return e;
     smem_set[dev] = true;
   }
-  return launch_cluster(commit_cluster_kernel<kFused>, C, 1, kCThreads, smem, s, a, slots, per, npm, f);
+  return launch_cluster(commit_cluster_kernel<kFused, kKv4>, C, 1, kCThreads, smem, s, a, slots, per, npm, f);
 }
 
 cudaError_t launch_commit(const CommitArgs& a, const GreedyAcceptArgs* fused, cudaStream_t s) {
-  if (fused) return launch_commit_t<true>(a, *fused, s);
-  return launch_commit_t<false>(a, GreedyAcceptArgs{}, s);
+  if (fused) return launch_commit_t<true, false>(a, *fused, s);   // (no fused form of the 4-bit commit)
+  if (a.kv4) return launch_commit_t<false, true>(a, GreedyAcceptArgs{}, s);
+  return launch_commit_t<false, false>(a, GreedyAcceptArgs{}, s);
 }
 
 }  // namespace tidar
