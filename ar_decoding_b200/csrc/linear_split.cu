@@ -20,7 +20,7 @@
 // warps with four in flight took 7 us over 136 rows of two splits).  Rows, features
 // and the reduction may end anywhere (TMA reads zeros outside).
 //
-// 272 x 4096 x 4096 with a residual: 17.2 us (0.53 PFLOP/s, 2.3 TB/s; the paired tiles
+// 272 x 4096 x 4096 with a residual: 16.9 us (0.54 PFLOP/s, 2.4 TB/s; the paired tiles
 // of linear_pair.cu 27); 1 x 16384 x 4096: 28.4 us, 4.7 TB/s; 77 x 1000 x 1544: 8.5 us,
 // of which about 7 pass before the first product and after the last (launch,
 // cluster, TMEM, the first loads; the exchange of the partial sums).
@@ -119,7 +119,11 @@ __device__ __forceinline__ void reduce_rows(const SplitParams& prm, uint32_t sb,
       for (int q = 1; q < KS; ++q)
         if (q < prm.ks) o[0] += v[u][q].x, o[1] += v[u][q].y, o[2] += v[u][q].z, o[3] += v[u][q].w;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = lin_act(o[e] + b4[e], prm.act);
+      for (int e = 0; e < 4; ++e) o[e] += b4[e];
+      if (prm.act != TIDAR_ACT_NONE) {
+        const float4 r = lin_act4(make_float4(o[0], o[1], o[2], o[3]), prm.act);
+        o[0] = r.x; o[1] = r.y; o[2] = r.z; o[3] = r.w;
+      }
       __nv_bfloat16* y = prm.y + (size_t)(t0 + t) * prm.N + f0;
       if (vec) {
         if (prm.residual) {
