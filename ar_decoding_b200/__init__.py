@@ -793,6 +793,10 @@ def build_tables(page_table, ctx_lens, new_lens, pool, *, page_size, num_pages, 
         _shaped(sta, "row_starts", (B + 1,), torch.int32, dev)
         _shaped(slo, "slots", (max_rows,), torch.int64, dev)
         _shaped(pos, "positions", (max_rows,), torch.int32, dev)
+    if not B:                                # the library writes nothing: no rows, no pages
+        if cnt is not fc:
+            cnt.copy_(fc)
+        sta.zero_(), slo.fill_(-1), pos.fill_(-1)
     d = TablesDesc(B, int(page_size), int(num_pages), width, max_rows)
     p = PagePool(fp.data_ptr() or None, fc.data_ptr(), fp.numel())
     st = lib().tidar_build_tables(ctypes.byref(d), page_table.data_ptr(), ctx_lens.data_ptr(), new_lens.data_ptr(),
@@ -1014,6 +1018,8 @@ def commit_kv4(cache, accept_count, k, *, head_dim, max_prefix_len, released=Non
         num_released = accept_count.new_empty((1,))
     _shaped(released, "released", (cap,), torch.int32, dev)
     _shaped(num_released, "num_released", (1,), torch.int32, dev)
+    if not B:                                # the library writes nothing
+        num_released.zero_()
     st = lib().tidar_commit_kv4(ctypes.byref(desc), ctypes.byref(cdesc), accept_count.data_ptr(),
                                 released.data_ptr(), num_released.data_ptr(), _raw_stream(dev.index))
     if st:

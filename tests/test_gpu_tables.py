@@ -107,6 +107,19 @@ def test_empty_batch_is_a_noop():
     assert out["page_table"].shape == (0, 4) and tidar.device_status() == (tidar.OK, 0)
 
 
+def test_empty_batch_has_no_rows():
+    z = torch.zeros(0, dtype=torch.int32, device="cuda")
+    pool = dict(free_pages=dev([1, 0]), free_count=dev([2]))
+    torch.full((64,), 7, device="cuda")                  # what the call is given to allocate is not zeros
+    out = tidar.build_tables(torch.zeros(0, 4, dtype=torch.int32, device="cuda"), z, z, pool, page_size=16, num_pages=2,
+                             max_rows=5)
+    assert out["free_count"].tolist() == [2] and out["row_starts"].tolist() == [0]
+    assert out["slots"].tolist() == [-1] * 5 and out["positions"].tolist() == [-1] * 5
+    cache = tidar.kv4_cache(2, 2, 16, 64, out["page_table"], z)
+    assert tidar.commit_kv4(cache, z, 4, head_dim=64, max_prefix_len=16, num_released=dev([9]))[1].tolist() == [0]
+    assert tidar.device_status() == (tidar.OK, 0)
+
+
 def test_captured_and_on_another_stream():
     st = state(4, 40, 16, 200, 30)
     rows = int(st["new"].sum()) + 3
