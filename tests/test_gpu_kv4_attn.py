@@ -312,3 +312,35 @@ def test_values_at_the_ends_of_the_range_are_exact(k, magnitude):
         out, _ = tidar.step_attn_kv4(q, blk, blk, cache, k, max_prefix_len=1, step_keys=False, append=False, path=path)
         assert torch.equal(out, want[0].repeat_interleave(2, 0).expand(1, R, 2 * H, D)), path
     assert tidar.device_status() == (tidar.OK, 0)
+
+
+def test_offsets_past_32_bits():
+    # pages at both ends of 4.7 GB a tensor; every path, append, read back and commit
+    H, D, ps, pages = 2, 128, 128, 256000
+    assert pages * H * tidar.kv4_page_bytes(ps, D) > 2 ** 32
+    used = [pages - 1, 0, pages - 7]
+    table = torch.tensor([used + [-1]], dtype=torch.int32, device="cuda")
+    small = torch.tensor([[2, 0, 1, -1]], dtype=torch.int32, device="cuda")
+    P, k = 300, 4
+    caches = [tidar.kv4_cache(n, H, ps, D, t, torch.tensor([P], dtype=torch.int32, device="cuda"))
+              for n, t in ((pages, table), (3, small))]
+    g = torch.Generator(device="cuda").manual_seed(8)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    rows, pos = (rnd(P, H, D), rnd(P, H, D)), torch.arange(P, device="cuda")
+    slots = [c["page_table"][0, pos // ps].long() * ps + pos % ps for c in caches]
+    for c, s in zip(caches, slots):
+        tidar.kv4_append(c, *rows, s)
+    back = [tidar.kv4_gather(c, s, head_dim=D) for c, s in zip(caches, slots)]
+    assert torch.equal(back[0][0], back[1][0]) and torch.equal(back[0][1], back[1][1]) and (back[0][0] != 0).any()
+    for kk in (0, k):
+        R = 1 if kk == 0 else kk + kk * kk
+        q, kb, vb = rnd(1, R, 2 * H, D), rnd(1, R, H, D), rnd(1, R, H, D)
+        for path in paths(kk, 2, D, "bf16"):
+            got = [tidar.step_attn_kv4(q, kb, vb, c, kk, max_prefix_len=P, path=path) for c in caches]
+            assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1]), path
+    for c in caches:
+        tidar.commit_kv4(c, torch.ones(1, dtype=torch.int32, device="cuda"), k, head_dim=D, max_prefix_len=P)
+    for n in ("k_pages", "v_pages"):
+        assert torch.equal(caches[0][n][torch.tensor(used, device="cuda")], caches[1][n][torch.tensor([2, 0, 1], device="cuda")])
+        assert not caches[0][n][1:pages - 7].any()         # nothing went anywhere else
+    assert tidar.device_status() == (tidar.OK, 0)
