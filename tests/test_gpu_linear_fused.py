@@ -137,3 +137,17 @@ def test_two_streams_and_capture():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for y in got) and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("N", [65536, 65537])
+def test_outputs_past_32_bits(N):
+    T, K = 33000, 8
+    assert T * N > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(N)
+    # whole numbers: products and sums are exact, so the order of the sums is no matter
+    x = torch.randint(-3, 4, (T, K), generator=g, device="cuda").bfloat16()
+    w = torch.randint(-3, 4, (N, K), generator=g, device="cuda").bfloat16()
+    y = tidar.linear_fused(x, w, activation="relu")
+    for r in (0, 255, 32767, 32768, 32999):
+        assert torch.equal(y[r].float(), torch.relu(w.float() @ x[r].float())), r
+    assert torch.equal(y[:, N - 1].float(), torch.relu(x.float() @ w[N - 1].float()))
