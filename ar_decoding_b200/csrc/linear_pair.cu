@@ -174,7 +174,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         if (ok) commit_pair(bar(BAR_ACC + buf), (uint16_t)3);
       }
     }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------------- epilogue
     const int q4 = warp & 3;       // TMEM lane quarter
@@ -193,6 +192,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 #pragma unroll 1
       for (int c = c0; c < c1; c += 32) {
         uint32_t acc[32];
+        // the stores of the 32 columns before this may have parted the warp (rows past
+        // T, features past N), and the load wants it whole
+        __syncwarp();
         tc05::tmem_ld32(src + (uint32_t)c, acc);
         tc05::tmem_wait_ld();
         if (c + 32 == c1) {        // this share of the accumulator has been read: the next tile may overwrite it
@@ -245,6 +247,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     }
   }
   // No MMA, copy or remote arrival is left when a CTA of the pair exits.
+  __syncwarp();                    // the roles parted the warps; the cluster barrier and the release want them whole
   tc05::fence_before();
   __syncthreads();
   cluster_sync_all();

@@ -151,3 +151,18 @@ def test_outputs_past_32_bits(N):
     for r in (0, 255, 32767, 32768, 32999):
         assert torch.equal(y[r].float(), torch.relu(w.float() @ x[r].float())), r
     assert torch.equal(y[:, N - 1].float(), torch.relu(x.float() @ w[N - 1].float()))
+
+
+@pytest.mark.parametrize("T", [4097, 4103, 4127])
+@pytest.mark.parametrize("N,K", [(2048, 512), (2056, 200)])
+def test_ragged_rows_on_the_paired_tiles(T, N, K):
+    # Rows that end inside a warp's 32 while N % 8 == 0: some lanes of the last row tile
+    # store nothing between two loads of the whole warp.  The paired tiles take these
+    # sizes: 136 or 153 tiles are three waves of 74 pairs at most, 16000 + 3 * 8 * 760 =
+    # 34000 clocks; the split kernel's 88 tiles or more are two waves of 24000 at least
+    # (6000 + 55 a row of 320), before a slice is counted.
+    x, w, b, r = data(T + N, T, N, K)
+    flat = torch.full((T * N + 64,), 77.0, dtype=torch.bfloat16, device="cuda")
+    y = tidar.linear_fused(x, w, bias=b, activation="silu", residual=r, out=flat[:T * N].view(T, N))
+    check(y, *reference(x, w, b, "silu", r))
+    assert (flat[T * N:] == 77).all() and tidar.device_status() == (tidar.OK, 0)
