@@ -999,6 +999,7 @@ __device__ __forceinline__ void attn_body(const CUtensorMap& tm_q, const CUtenso
 #endif
   }
   if (warp == L::kMma) {
+    __syncwarp();          // the append parts the warp (rows past n, unmapped pages); the release wants it whole
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }

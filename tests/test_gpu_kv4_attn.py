@@ -344,3 +344,16 @@ def test_offsets_past_32_bits():
         assert torch.equal(caches[0][n][torch.tensor(used, device="cuda")], caches[1][n][torch.tensor([2, 0, 1], device="cuda")])
         assert not caches[0][n][1:pages - 7].any()         # nothing went anywhere else
     assert tidar.device_status() == (tidar.OK, 0)
+
+
+@pytest.mark.parametrize("k", [0, 1, 2, 4])
+def test_many_calls_whose_append_leaves_lanes_idle(k):
+    # 2n units of four lanes: with n = 1 or 2 most lanes of the warp that releases the
+    # tensor memory store nothing.  As many calls as several rounds of the device's SMs,
+    # each of which has to find all of it free again.
+    st = make(61, [40] * 24, 8, 4, 128, k, 64, "bf16")
+    want = run(st, "tc05")
+    for _ in range(40):
+        got = run(st, "tc05", append=True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    compare(st, *got, seqs=[0, 23])
