@@ -79,15 +79,26 @@ __global__ void __launch_bounds__(kWarps * 32) attn_simt_kernel(AttnArgs a) {
 #pragma unroll
     for (int u = 0; u < kKB; ++u)
       if (ok[u]) mn = fmaxf(mn, sc[u]);
-    if (mn == -INFINITY) return;                    // no key in the batch (and none before)
-    const float corr = expf(mx - mn);               // 0 while mx = -inf
+    float off = mn;                                 // of the exponents
+    if constexpr (KV4) {
+      // fmaxf passes over NaN, so keys whose scores are all NaN leave no maximum
+      // either: they count, with the offset 0 (expf of a NaN reaches l and acc)
+      bool any = false;
+#pragma unroll
+      for (int u = 0; u < kKB; ++u) any = any || ok[u];
+      if (!any) return;
+      if (mn == -INFINITY) off = 0.f;
+    } else if (mn == -INFINITY) {
+      return;                                       // no key in the batch (and none before)
+    }
+    const float corr = expf(mx - off);              // 0 while mx = -inf
     float ps = 0.f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) acc[i] *= corr;
 #pragma unroll
     for (int u = 0; u < kKB; ++u) {
       if (!ok[u]) continue;                          // its K/V registers were never loaded
-      const float pe = expf(sc[u] - mn);
+      const float pe = expf(sc[u] - off);
       ps += pe;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) acc[i] = fmaf(pe, vv[u][i], acc[i]);
