@@ -210,6 +210,9 @@ __global__ void __launch_bounds__(kWarps * 32) finalize_kernel(AttnArgs a, int m
     float acc[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
+    // KV4: the splits that saw a key.  Their rows count at a weight that came out as 0
+    // too: 0 times a NaN value is NaN, as it is within a split.
+    const unsigned live_a = __ballot_sync(0xffffffffu, la != -INFINITY), live_b = __ballot_sync(0xffffffffu, lb != -INFINITY);
     float wa = 0.f, wb = 0.f, mx = -INFINITY, wsum = 0.f;
     for (int s0 = 0; s0 < ns; s0 += kFinChunk) {
       float v[kFinChunk][VPL];
@@ -231,7 +234,8 @@ __global__ void __launch_bounds__(kWarps * 32) finalize_kernel(AttnArgs a, int m
       for (int u = 0; u < kFinChunk; ++u) {
         const int sp = s0 + u;
         const float w = __shfl_sync(0xffffffffu, sp < 32 ? wa : wb, sp & 31);
-        if (sp < ns && (KV4 ? w != 0.f : w > 0.f)) {
+        const bool live = ((sp < 32 ? live_a : live_b) >> (sp & 31)) & 1u;
+        if (sp < ns && (KV4 ? live : w > 0.f)) {
 #pragma unroll
           for (int i = 0; i < VPL; ++i) acc[i] = fmaf(w, v[u][i], acc[i]);
         }

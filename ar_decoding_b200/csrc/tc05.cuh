@@ -378,7 +378,7 @@ __device__ __forceinline__ void merge_rows_t(const float* ost, const float* lst,
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const float ws = __shfl_sync(kAll, w[u], (s0 + j) & 31);
-          if (s0 + j < ns && (kNan ? ws != 0.f : ws > 0.f)) {
+          if (s0 + j < ns && (kNan || ws > 0.f)) {
             acc[u].x = fmaf(ws, x[u][j].x, acc[u].x); acc[u].y = fmaf(ws, x[u][j].y, acc[u].y);
             acc[u].z = fmaf(ws, x[u][j].z, acc[u].z); acc[u].w = fmaf(ws, x[u][j].w, acc[u].w);
           }
@@ -402,8 +402,9 @@ __device__ __forceinline__ void merge_rows_t(const float* ost, const float* lst,
 
 // This CTA's share of the merge: U rows per warp (at most kMaxU), NC splits'
 // rows in flight per chunk, U picked so that the block's warps take all
-// `owned` rows in one pass where they can (ns <= 32).  kNan: a split whose lse is
-// NaN makes the row NaN (else it gets no weight).
+// `owned` rows in one pass where they can (ns <= 32).  kNan: a NaN survives the merge,
+// be it a split's lse or a value in a split whose weight comes out as 0: no row is
+// selected away, and a split that saw no key has staged zeros.
 template <int kMaxU, int NC, bool kNan = false, class RowOf>
 __device__ __forceinline__ void merge_rows(const float* ost, const float* lst, int ns, int rank, int owned,
                                            RowOf out_row, __nv_bfloat16* out, float* lse_out) {

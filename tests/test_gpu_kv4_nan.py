@@ -84,3 +84,37 @@ def test_nan_in_a_key_that_a_row_does_not_see(dtype, D, k):
         out, lse = call(st, path)
         assert torch.isnan(out[:, -k:]).all() and torch.isnan(lse[:, -k:]).all(), path
         assert torch.isfinite(out[:, :-k]).all() and torch.isfinite(lse[:, :-k]).all(), path
+
+
+@pytest.mark.parametrize("force", [0, 1])
+@pytest.mark.parametrize("P", [64, 600, 4096])
+@pytest.mark.parametrize("k", [0, 4])
+@pytest.mark.parametrize("dtype,D", TYPES)
+def test_nan_value_of_a_key_whose_weight_is_nothing(dtype, D, k, P, force):
+    # Scores are 200 in the second half of the prefix and -200 in the first, so the first
+    # half's weight is exp(-400) = 0 in fp32, as are the weights of the splits that hold
+    # it; the definition's 0 * NaN is NaN all the same, in that group of that head.
+    ps, H, B = 16, 2, 2
+    table = torch.arange(B * (P // ps + 2), dtype=torch.int32, device="cuda").view(B, -1)
+    cache = tidar.kv4_cache(table.numel(), H, ps, D, table, torch.full((B,), P, dtype=torch.int32, device="cuda"))
+    sign = torch.where(torch.arange(P, device="cuda") < P // 2, -1.0, 1.0)[None, :, None, None]
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    rows = (sign * torch.ones(B, P, H, D, device="cuda")).to(dt)
+    vals = torch.randn(B, P, H, D, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5)).to(dt)
+    pos = torch.arange(P, device="cuda")
+    slots = (table.long()[:, pos // ps] * ps + pos % ps).reshape(-1)
+    tidar.kv4_append(cache, rows.reshape(-1, H, D), vals.reshape(-1, H, D), slots)
+    st = dict(cache=cache, table=table, ps=ps, D=D, k=k, P=[P] * B)
+    poison(st, "v_pages", 1, [P // 4], 1, group=1)
+    R = 1 if k == 0 else k + k * k
+    st["q"] = torch.full((B, R, 2 * H, D), 200 / math.sqrt(D), device="cuda").to(dt)
+    st["k_blk"] = st["v_blk"] = torch.zeros(B, R, H, D, dtype=dt, device="cuda")
+    tidar.debug_set(tidar.DEBUG_FORCE_SPLIT_PARTIALS, force)
+    try:
+        for path in paths(k, 2, D, dtype):
+            out, lse = call(st, path)
+            hit = torch.zeros_like(out, dtype=torch.bool)
+            hit[1, :, 2:, 32:64] = True
+            assert (torch.isnan(out) == hit).all() and torch.isfinite(lse).all(), path
+    finally:
+        tidar.debug_set(tidar.DEBUG_FORCE_SPLIT_PARTIALS, 0)
