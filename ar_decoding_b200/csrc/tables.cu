@@ -470,6 +470,33 @@ __global__ void __launch_bounds__(kFThreads) fused_kernel(TablesArgs a, int entr
   if (bad) raise_error(a.err, TIDAR_DEVERR_BAD_PAGE);
 }
 
+// Shared memory of a call, in bytes, and the most that any call takes.
+constexpr size_t fused_smem(long long B, long long entries) {
+  return (5 * (size_t)B + 2 + (size_t)entries + 2 * (((size_t)entries + 31) / 32)) * sizeof(int);
+}
+constexpr size_t tables_smem(int per) { return (size_t)per * sizeof(TabRec); }
+constexpr size_t kFusedSmemMax = fused_smem(kFusedBatch, kFusedEntries);
+constexpr size_t kTablesSmemMax = tables_smem(kTablesMaxBatch / kTMaxCluster);
+static_assert(kFusedSmemMax + 1024 <= 232448 && kTablesSmemMax + 1024 <= 232448, "shared memory budget");
+
+// A kernel's opt-in is the function's, shared by all host threads and captured
+// calls: set to the most once per device, never to one call's size.
+cudaError_t smem_attr() {
+  static bool set[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorNotSupported;
+  if (!set[dev]) {
+    e = cudaFuncSetAttribute(fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFusedSmemMax);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTablesSmemMax);
+    if (e != cudaSuccess) return e;
+    set[dev] = true;
+  }
+  return cudaSuccess;
+}
+
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 }  // namespace
@@ -503,31 +530,23 @@ extern "C" tidar_status tidar_build_tables(const tidar_tables_desc* d, const int
   a.starts = row_starts; a.slots = slots; a.positions = positions;
   const tidar_status st = error_word_status(&a.err);
   if (st != TIDAR_OK) return st;
+  if (const cudaError_t e = smem_attr(); e != cudaSuccess) return cuda_status(e);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // Entries in use: a sequence of m > 0 rows uses at most m / ps + 2.  In place the
   // CTAs of one launch would read what others have already written.
   const long long entries = a.max_rows / a.ps + 2LL * a.B;
   if (a.B <= kFusedBatch && entries <= kFusedEntries && a.table_in != a.table_out && a.free_count != a.count_out) {
-    const size_t smem = (5 * (size_t)a.B + 2 + (size_t)entries + 2 * ((entries + 31) / 32)) * sizeof(int);
-    cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024) e = cudaFuncSetAttribute(fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return cuda_status(e);
+    const size_t smem = fused_smem(a.B, entries);
     // a CTA per 1024 rows or per table row, up to one an SM
     const long long want = std::max<long long>(((long long)a.max_rows + 2 * kFThreads - 1) / (2 * kFThreads), a.B);
-    e = launch_pdl(fused_kernel, dim3((unsigned)std::min<long long>(std::max<long long>(want, 1), 148)), kFThreads, smem, s, a,
-                   (int)entries);
+    const cudaError_t e = launch_pdl(fused_kernel, dim3((unsigned)std::min<long long>(std::max<long long>(want, 1), 148)),
+                                     kFThreads, smem, s, a, (int)entries);
     return e == cudaSuccess ? TIDAR_OK : cuda_status(e);
   }
   // one warp per sequence, up to the portable cluster
   const int C = std::min(kTMaxCluster, (a.B + kTWarps - 1) / kTWarps);
   const int per = (a.B + C - 1) / C;
-  const size_t smem = (size_t)per * sizeof(TabRec);
-  cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return cuda_status(e);
-  }
-  e = launch_cluster(tables_kernel, C, 1, kTThreads, smem, s, a, per);
+  cudaError_t e = launch_cluster(tables_kernel, C, 1, kTThreads, tables_smem(per), s, a, per);
   if (e != cudaSuccess) return cuda_status(e);
   if (a.max_rows > 0) {
     const long long pairs = ((long long)a.max_rows + 1) / 2;

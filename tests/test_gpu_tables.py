@@ -1,4 +1,7 @@
 """tidar_build_tables against its definition (integers: exact)."""
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -138,3 +141,57 @@ def test_captured_and_on_another_stream():
     torch.cuda.synchronize()
     for k in want:
         assert torch.equal(want[k], other[k]) and torch.equal(want[k], out[k]), k
+
+
+@pytest.mark.parametrize("sizes", [((4, 250000), (4, 205000)), ((60000, 60000), (20000, 20000))])
+def test_two_host_threads_and_two_sizes_of_shared_memory(sizes):
+    # Both sizes of a pair take more shared memory than a launch gets unasked (48 KB):
+    # 15633 and 12821 table entries in the one-launch form, 7500 and 2500 sequences a CTA
+    # in the other.  Two threads call the library at once, each on its own stream and
+    # with its own results; no call may depend on what the other's asked for.
+    def inputs(B, rows):
+        ps, each = 16, rows // B
+        need, width = B * -(-each // ps), -(-each // ps) + 1
+        t = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+        pool = dict(free_pages=torch.arange(need, dtype=torch.int32, device="cuda"), free_count=dev([need]))
+        ctx, new = dev(np.zeros(B)), dev(np.full(B, each))
+        kw = dict(page_size=ps, num_pages=need, max_rows=B * each)
+        want = tidar.build_tables(t, ctx, new, pool, **kw)
+        out = {n: torch.empty_like(w) for n, w in want.items()}
+        d = tidar.TablesDesc(B, ps, need, width, B * each)
+        p = tidar.PagePool(pool["free_pages"].data_ptr(), pool["free_count"].data_ptr(), need)
+
+        def raw(stream):                                   # the call alone, as another language's program makes it
+            return tidar.lib().tidar_build_tables(
+                ctypes.byref(d), t.data_ptr(), ctx.data_ptr(), new.data_ptr(), ctypes.byref(p),
+                *(out[n].data_ptr() for n in ("page_table", "free_count", "row_starts", "slots", "positions")), stream)
+        raw.keep = (t, pool, ctx, new)
+        return raw, out, want, lambda: tidar.build_tables(t, ctx, new, pool, **kw)
+
+    calls = [inputs(*s) for s in sizes]
+    torch.cuda.synchronize()
+    status, start = [set(), set()], threading.Barrier(2)
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        start.wait()
+        for _ in range(10000):
+            status[i].add(calls[i][0](stream.cuda_stream))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert status == [{tidar.OK}, {tidar.OK}], status
+    for _, out, want, _ in calls:
+        assert all(torch.equal(out[n], want[n]) for n in want)
+    # and both in one graph, the smaller last
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = [c[3]() for c in calls]
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a[n], c[2][n]) for a, c in zip(got, calls) for n in a)
+    assert tidar.device_status() == (tidar.OK, 0)
