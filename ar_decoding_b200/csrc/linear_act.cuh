@@ -5,12 +5,35 @@
 
 namespace tidar {
 
+// v Phi(v), Phi the normal distribution function (0.5 (1 + erf(v / sqrt 2)), without
+// that sum's cancellation in the negative tail: 1 + erff has one digit left at v = -5 and
+// none below -5.6).  Phi(-t) = exp(-t^2 / 2) G(t) for t >= 0, and G(t) = erfcx(t / sqrt 2)
+// / 2 falls slowly, like 1 / t: a polynomial in s = 1 / (1 + t / 3.4), fitted by least
+// squares to the smallest relative error on 0 <= t <= 13.6 (3.6e-8; Phi(-13.6) is below
+// bf16's range).  The result is off by 5e-7 of itself for |v| < 1, 3e-6 down to -8 and
+// 8e-6 to -13 (the exponent's rounding).  1024 x 4096 x 4096: 32.8 us with erff, 31.9 with
+// this, 35.6 with erfcf.
+__device__ __forceinline__ float lin_gelu(float v) {
+  const float t = fabsf(v), s = __fdividef(1.f, fmaf(t, 1.f / 3.4f, 1.f));
+  float g = 0.039509729f;
+  g = fmaf(g, s, -0.185585514f);
+  g = fmaf(g, s, 0.278201669f);
+  g = fmaf(g, s, -0.124241441f);
+  g = fmaf(g, s, 0.170618534f);
+  g = fmaf(g, s, 0.0828891173f);
+  g = fmaf(g, s, 0.121692568f);
+  g = fmaf(g, s, 0.116896264f);
+  g = fmaf(g, s, 1.90702776e-5f);
+  const float q = g * __expf(-0.5f * t * t);
+  return v * (v < 0.f ? q : 1.f - q);
+}
+
 // On the fp32 sum (bias added).  v / (1 + exp(-u)) is 0 once exp overflows, v
 // once it vanishes; a NaN stays a NaN.
 __device__ __forceinline__ float lin_act(float v, int act) {
   switch (act) {
     case TIDAR_ACT_RELU: return v < 0.f ? 0.f : v;
-    case TIDAR_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+    case TIDAR_ACT_GELU: return lin_gelu(v);
     // 0.5 v (1 + tanh u) = v / (1 + exp(-2u)): no cancellation in the negative tail
     case TIDAR_ACT_GELU_TANH: {
       const float u2 = 1.5957691216057308f * fmaf(0.044715f * v * v, v, v);

@@ -166,3 +166,38 @@ def test_ragged_rows_on_the_paired_tiles(T, N, K):
     y = tidar.linear_fused(x, w, bias=b, activation="silu", residual=r, out=flat[:T * N].view(T, N))
     check(y, *reference(x, w, b, "silu", r))
     assert (flat[T * N:] == 77).all() and tidar.device_status() == (tidar.OK, 0)
+
+
+def act_of_every_bf16(act, T):
+    """activation(b) of every finite bf16 number b, by x = 0 and the bias, and of the
+    definition in 64 bits, written without cancellation."""
+    b = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16)
+    b = b[torch.isfinite(b)].contiguous()
+    x, w = (torch.zeros(n, 8, dtype=torch.bfloat16, device="cuda") for n in (T, b.numel()))
+    # one row: a few thousand features a call, which the split kernel takes; 2048 rows of
+    # all of them are the paired tiles'
+    y = torch.cat([tidar.linear_fused(x, w[:c.numel()], bias=c.clone(), activation=act)
+                   for c in b.split(4080 if T == 1 else b.numel())], 1)
+    assert (y == y[:1]).all()
+    v = b.double()
+    if act == "gelu":
+        want = 0.5 * v * torch.erfc(v * -math.sqrt(0.5))
+    else:
+        u = v if act == "silu" else 2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)
+        e = torch.exp(-u.abs())
+        want = torch.where(u < 0, v * e, v) / (1 + e)
+    return v, y[0].double(), want
+
+
+# Relative error: half a step of bf16, 2^-8, and the fp32 evaluation.  A factor exp(-z)
+# carries z's rounding times z, and an activation's value is above 2^-133 only for z < 93;
+# three roundings of z and 110 units of the exponential's own are (3 * 93 + 110) 2^-24 <
+# 2^-15.  Below bf16's normal numbers half a step is 2^-134.
+TAIL_REL, TAIL_ABS = 2.0 ** -8 + 2.0 ** -15, 2.0 ** -133
+
+
+@pytest.mark.parametrize("T", [1, 2048])
+def test_erf_gelu_of_every_bf16_number(T):
+    v, y, want = act_of_every_bf16("gelu", T)
+    bad = (y - want).abs() > TAIL_REL * want.abs() + TAIL_ABS
+    assert not bad.any(), v[bad]
