@@ -28,8 +28,15 @@ __device__ __forceinline__ float lin_gelu(float v) {
   return v * (v < 0.f ? q : 1.f - q);
 }
 
-// On the fp32 sum (bias added).  v / (1 + exp(-u)) is 0 once exp overflows, v
-// once it vanishes; a NaN stays a NaN.
+// v / (1 + exp(-u)).  The exponential of -|u| does not overflow and the quotient's
+// denominator stays in 1 .. 2, so the negative tail, v exp(u), is kept to the end of the
+// range (__fdividef is 0 past a denominator of 2^126: u < -87.3).
+__device__ __forceinline__ float lin_sigmoid_of(float v, float u) {
+  const float e = __expf(-fabsf(u));
+  return __fdividef(u < 0.f ? v * e : v, 1.f + e);
+}
+
+// On the fp32 sum (bias added); a NaN stays a NaN.
 __device__ __forceinline__ float lin_act(float v, int act) {
   switch (act) {
     case TIDAR_ACT_RELU: return v < 0.f ? 0.f : v;
@@ -37,9 +44,9 @@ __device__ __forceinline__ float lin_act(float v, int act) {
     // 0.5 v (1 + tanh u) = v / (1 + exp(-2u)): no cancellation in the negative tail
     case TIDAR_ACT_GELU_TANH: {
       const float u2 = 1.5957691216057308f * fmaf(0.044715f * v * v, v, v);
-      return __fdividef(v, 1.f + __expf(-u2));
+      return lin_sigmoid_of(v, u2);
     }
-    case TIDAR_ACT_SILU: return __fdividef(v, 1.f + __expf(-v));
+    case TIDAR_ACT_SILU: return lin_sigmoid_of(v, v);
   }
   return v;
 }

@@ -201,3 +201,11 @@ def test_erf_gelu_of_every_bf16_number(T):
     v, y, want = act_of_every_bf16("gelu", T)
     bad = (y - want).abs() > TAIL_REL * want.abs() + TAIL_ABS
     assert not bad.any(), v[bad]
+
+
+@pytest.mark.parametrize("T", [1, 2048])
+@pytest.mark.parametrize("act", ["gelu_tanh", "silu"])
+def test_sigmoid_forms_of_every_bf16_number(act, T):
+    v, y, want = act_of_every_bf16(act, T)
+    bad = (y - want).abs() > TAIL_REL * want.abs() + TAIL_ABS
+    assert not bad.any(), v[bad]
