@@ -253,16 +253,20 @@ def make_desc(q, k_blk, cache, k, max_prefix_len, scale=0.0, path="auto") -> Ste
                     dtype=_dtype_code(q), softmax_scale=float(scale), path=_PATHS[path])
 
 
-def make_cache_desc(cache, device=None) -> KVCacheDesc:
+def make_cache_desc(cache, device=None, batch=None) -> KVCacheDesc:
+    """Descriptor of `cache` for a call on `batch` sequences (None: as many as seq_lens)."""
     for n in ("k_pages", "v_pages", "page_table", "seq_lens"):
         _dev(cache[n], n, None, device)
-    if cache["page_table"].dtype != torch.int32 or cache["seq_lens"].dtype != torch.int32:
+    table, lens = cache["page_table"], cache["seq_lens"]
+    if table.dtype != torch.int32 or lens.dtype != torch.int32:
         raise ValueError("page_table and seq_lens must be int32")
+    batch = lens.numel() if batch is None else batch
+    if table.dim() < 2 or table.shape[0] < batch or lens.numel() < batch:
+        raise ValueError(f"page_table {tuple(table.shape)} and seq_lens {tuple(lens.shape)} must hold a row of pages "
+                         f"and a length for each of {batch} sequences")
     return KVCacheDesc(k_pages=cache["k_pages"].data_ptr(), v_pages=cache["v_pages"].data_ptr(),
-                       page_table=cache["page_table"].data_ptr(),
-                       seq_lens=cache["seq_lens"].data_ptr(),
-                       num_pages=cache["k_pages"].shape[0],
-                       max_pages_per_seq=cache["page_table"].shape[1])
+                       page_table=table.data_ptr(), seq_lens=lens.data_ptr(),
+                       num_pages=cache["k_pages"].shape[0], max_pages_per_seq=table.shape[1])
 
 
 def plan(desc: StepDesc) -> tuple[int, int]:
@@ -290,7 +294,7 @@ def step_attn(q, k_blk, v_blk, cache, k, *, max_prefix_len, scale=0.0, path="aut
     _dev(k_blk, "k_blk", q.dtype, dev)
     _dev(v_blk, "v_blk", q.dtype, dev)
     desc = make_desc(q, k_blk, cache, k, max_prefix_len, scale, path)
-    cdesc = make_cache_desc(cache, dev)
+    cdesc = make_cache_desc(cache, dev, desc.batch)
     if cache["k_pages"].dtype != q.dtype or cache["v_pages"].dtype != q.dtype:
         raise ValueError("the cache pages must have q's dtype")
     if out is None:
@@ -396,7 +400,7 @@ def layer_step(x, w_qkv, w_o, cache, k, num_q_heads, num_kv_heads, *, max_prefix
     B, R, dm = x.shape
     desc = _layer_desc(x, k, num_q_heads, num_kv_heads, max_prefix_len,
                        page_size=cache["k_pages"].shape[2], path=path)
-    cdesc = make_cache_desc(cache, dev)
+    cdesc = make_cache_desc(cache, dev, desc.batch)
     if out is None:
         out = torch.empty((B, R, dm), dtype=torch.bfloat16, device=dev)
     if lse is None and want_lse:
@@ -424,7 +428,7 @@ def step_attn_part(q, k_blk, v_blk, cache, k, flags, *, max_prefix_len, scale=0.
     _dev(k_blk, "k_blk", q.dtype, dev)
     _dev(v_blk, "v_blk", q.dtype, dev)
     desc = make_desc(q, k_blk, cache, k, max_prefix_len, scale, path)
-    cdesc = make_cache_desc(cache, dev)
+    cdesc = make_cache_desc(cache, dev, desc.batch)
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
@@ -621,7 +625,7 @@ def commit(cache, accept_count, k, *, max_prefix_len, head_dim=None, num_q_heads
     desc = StepDesc(batch=B, num_q_heads=num_q_heads or Hkv, num_kv_heads=Hkv, head_dim=D, k=k,
                     page_size=ps, max_prefix_len=int(max_prefix_len), dtype=_dtype_code(kp),
                     softmax_scale=0.0, path=PATH_AUTO)
-    cdesc = make_cache_desc(cache, kp.device)
+    cdesc = make_cache_desc(cache, kp.device, B)
     cap = B * ((n + ps - 1) // ps + 1)
     if released is None:
         released = torch.empty(cap, dtype=torch.int32, device=kp.device)
@@ -652,7 +656,7 @@ def verify_commit(logits, drafts, cache, k, mode="greedy", *, max_prefix_len, dr
     desc = StepDesc(batch=B, num_q_heads=Hkv, num_kv_heads=Hkv, head_dim=D, k=k, page_size=ps,
                     max_prefix_len=int(max_prefix_len), dtype=_dtype_code(kp), softmax_scale=0.0,
                     path=PATH_AUTO)
-    cdesc = make_cache_desc(cache, dev)
+    cdesc = make_cache_desc(cache, dev, desc.batch)
     if outputs is None:
         outputs = dict(accept_count=torch.empty(B, dtype=torch.int32, device=dev),
                        out_tokens=torch.empty((B, n), dtype=torch.int32, device=dev),
@@ -700,7 +704,7 @@ def reserve(cache, pool, k, *, max_prefix_len, returned=None, num_returned=None,
     desc = StepDesc(batch=B, num_q_heads=Hkv, num_kv_heads=Hkv, head_dim=D, k=k, page_size=ps,
                     max_prefix_len=int(max_prefix_len), dtype=dtype, softmax_scale=0.0,
                     path=PATH_AUTO)
-    cdesc = make_cache_desc(cache, kp.device)
+    cdesc = make_cache_desc(cache, kp.device, B)
     fp, fc = pool["free_pages"], pool["free_count"]
     _dev(fc, "free_count", torch.int32, kp.device)
     if fp.numel():
@@ -1009,7 +1013,7 @@ def commit_kv4(cache, accept_count, k, *, head_dim, max_prefix_len, released=Non
     ps = _kv4_page_size(cache, head_dim, dev)
     B, H, n = cache["seq_lens"].shape[0], kp.shape[1], max(k, 1)
     desc = StepDesc(B, H, H, head_dim, k, ps, int(max_prefix_len), BF16, 0.0, PATH_AUTO)
-    cdesc = make_cache_desc(cache, dev)
+    cdesc = make_cache_desc(cache, dev, desc.batch)
     _shaped(accept_count, "accept_count", (B,), torch.int32, dev)
     cap = B * ((n + ps - 1) // ps + 1)
     if released is None:

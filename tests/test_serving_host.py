@@ -178,3 +178,30 @@ def test_reference_layout_by_hand():
     assert k[2] == 7 and k[4 + 3] == 1 << 8 and np.count_nonzero(k[:16]) == 2
     assert v[1] == 7 and v[4 + 3] == 1 << 8 and np.count_nonzero(v[:16]) == 2
     assert k[16 * 16 + 1] == 0x3f80 and np.count_nonzero(k[16 * 16:]) == 1
+
+
+@pytest.mark.parametrize("bad", [dict(page_table=(1, 4)), dict(page_table=(8,)), dict(page_table=(0, 4))])
+def test_binding_refuses_tables_without_a_row_for_each_sequence(monkeypatch, bad):
+    # A table with fewer rows than there are lengths would be read past its end.  Host
+    # tensors stand in for device ones up to the library call, which is not reached.
+    monkeypatch.setattr(tidar, "_dev", lambda *a, **kw: None)
+    monkeypatch.setattr(tidar, "_away", lambda *a, **kw: False)
+    monkeypatch.setattr(tidar, "lib", lambda: pytest.fail("the library was called"))
+    shapes = dict(dict(page_table=(2, 4), seq_lens=(2,)), **bad)
+    common = {n: torch.zeros(v, dtype=torch.int32) for n, v in shapes.items()}
+    four = dict(common, **{n: torch.zeros(8, 2, 4608, dtype=torch.uint8) for n in ("k_pages", "v_pages")})
+    wide = dict(common, **{n: torch.zeros(8, 2, 64, 128, dtype=torch.bfloat16) for n in ("k_pages", "v_pages")})
+    pool = dict(free_pages=torch.arange(8, dtype=torch.int32), free_count=torch.tensor([8], dtype=torch.int32))
+    count = torch.zeros(2, dtype=torch.int32)
+    q, kv = torch.zeros(2, 1, 4, 128, dtype=torch.bfloat16), torch.zeros(2, 1, 2, 128, dtype=torch.bfloat16)
+    for call in (lambda: tidar.commit_kv4(four, count, 0, head_dim=128, max_prefix_len=8),
+                 lambda: tidar.reserve(four, pool, 0, max_prefix_len=8, head_dim=128),
+                 lambda: tidar.reserve(wide, pool, 0, max_prefix_len=8),
+                 lambda: tidar.commit(wide, count, 0, max_prefix_len=8),
+                 lambda: tidar.step_attn(q, kv, kv, wide, 0, max_prefix_len=8),
+                 lambda: tidar.step_attn_kv4(q, kv, kv, four, 0, max_prefix_len=8)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(ValueError):
+        tidar.step_attn(q, kv, kv, dict(wide, page_table=torch.zeros(2, 4, dtype=torch.int32), seq_lens=count[:1]), 0,
+                        max_prefix_len=8)
