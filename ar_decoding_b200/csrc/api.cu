@@ -265,8 +265,13 @@ int choose_path(const tidar_step_desc* d, bool kv4 = false) {
   return dec_supported(d, kv4) ? 3 : (tc05_supported(d, kv4) ? 2 : 1);
 }
 
+// The 4-bit kernels walk their keys in 32-bit integers, up to a few thousand past a
+// split's end.
+constexpr int kKv4MaxPrefix = 1 << 30;
+
 // Whether the family `path` takes this call.
 bool path_supported(const tidar_step_desc* d, int path, bool kv4) {
+  if (kv4 && d->max_prefix_len > kKv4MaxPrefix) return false;
   if (path == 4) return !kv4 && tc05_supported(d);
   return path == 1 || (path == 2 && tc05_supported(d, kv4)) || (path == 3 && dec_supported(d, kv4));
 }
@@ -279,7 +284,7 @@ size_t plan_workspace_bytes(const tidar_step_desc* d, const Plan& p) {
 }
 
 size_t step_workspace_bytes(const tidar_step_desc* d, bool kv4) {
-  if (check_desc(d) != TIDAR_OK) return 0;
+  if (check_desc(d) != TIDAR_OK || (kv4 && d->max_prefix_len > kKv4MaxPrefix)) return 0;
   return plan_workspace_bytes(d, make_plan(d, choose_path(d, kv4), kv4));
 }
 
@@ -636,6 +641,7 @@ tidar_status tidar_commit(const tidar_step_desc* d, const tidar_kv_cache* c,
 tidar_status tidar_commit_kv4(const tidar_step_desc* d, const tidar_kv_cache* c, const int32_t* accept_count,
                               int32_t* released_pages, int32_t* num_released, tidar_stream_t stream) {
   tidar::CommitArgs a{};
+  if (d && d->max_prefix_len > kKv4MaxPrefix) return TIDAR_ERR_UNSUPPORTED;
   const tidar_status st = commit_prepare(d, c, accept_count, released_pages, num_released, a, true);
   if (st != TIDAR_OK || d->batch == 0) return st;
   const cudaError_t e = tidar::launch_commit(a, nullptr, reinterpret_cast<cudaStream_t>(stream));

@@ -542,7 +542,8 @@ tidar_status tidar_build_tables(const tidar_tables_desc* desc, const int32_t* pa
  *   DEC (R * G <= 16) and TC05; PAIR is not offered.  A NaN among the values that a
  *   row attends makes the row's outputs NaN.  workspace as
  *   tidar_step_attn's, sized by tidar_step_attn_kv4_workspace_bytes.
- *   TIDAR_ERR_UNSUPPORTED when batch * num_kv_heads > 65535.
+ *   TIDAR_ERR_UNSUPPORTED when batch * num_kv_heads > 65535 or max_prefix_len >
+ *   2^30 (this one for tidar_commit_kv4 too).
  * tidar_commit_kv4: tidar_commit over such a cache (rejected rows are zeroed).
  * tidar_reserve and tidar_build_tables only touch the table and serve both.
  * ------------------------------------------------------------------------- */

@@ -205,3 +205,18 @@ def test_binding_refuses_tables_without_a_row_for_each_sequence(monkeypatch, bad
     with pytest.raises(ValueError):
         tidar.step_attn(q, kv, kv, dict(wide, page_table=torch.zeros(2, 4, dtype=torch.int32), seq_lens=count[:1]), 0,
                         max_prefix_len=8)
+
+
+def test_kv4_refuses_prefixes_past_its_indices(L):
+    # a table this wide is a legal argument; the kernels count keys in 32 bits
+    c = _cache(max_pages_per_seq=1 << 25)
+    for k in (0, 4, 16):
+        for path in range(4):
+            d = _desc(k=k, max_prefix_len=(1 << 30) + 1, path=path)
+            assert _attn(L, d, c, ws=FAKE, wsb=1 << 40) == tidar.ERR_UNSUPPORTED, (k, path)
+            assert L.tidar_step_attn_kv4_plan(ctypes.byref(d), None, None, None) == tidar.ERR_UNSUPPORTED
+            assert L.tidar_step_attn_kv4_workspace_bytes(ctypes.byref(d)) == 0
+        d = _desc(k=k, max_prefix_len=(1 << 30) + 1)
+        assert L.tidar_commit_kv4(ctypes.byref(d), c, FAKE, FAKE, FAKE, None) == tidar.ERR_UNSUPPORTED
+    d = _desc(max_prefix_len=1 << 30, path=tidar.PATH_SIMT)
+    assert L.tidar_step_attn_kv4_plan(ctypes.byref(d), None, None, None) == tidar.OK
