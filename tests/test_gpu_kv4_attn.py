@@ -357,3 +357,32 @@ def test_many_calls_whose_append_leaves_lanes_idle(k):
         got = run(st, "tc05", append=True)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     compare(st, *got, seqs=[0, 23])
+
+
+def compare_by_path(st, out, lse, path):
+    """compare() with what each kernel's own arithmetic warrants: the codes' offset of 136,
+    which widens compare()'s score term by 143/7, is the decode kernel's alone, and the
+    CUDA-core kernel rounds no p.  Sums over the keys add 2^-23 a step (16 keys a step in
+    the matrix products) of sum p|v|."""
+    D = st["D"]
+    q, kb, vb = (st[n].double().cpu().numpy() for n in ("q", "k_blk", "v_blk"))
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b in range(len(st["P"])):
+        wo, wl, spread, mag = kv4_ref.attention(q[b], kb[b], vb[b], st["pref"][0][b], st["pref"][1][b], st["k"])
+        keys = st["P"][b] + q.shape[1]
+        s_err = (D / 16 + 8) * 2.0 ** -23 * mag * (143 / 7 if path == "dec" else 1)
+        steps = keys if path == "simt" else keys / 16
+        tol = (2 * s_err + 2.0 ** -23 * (steps + 64)) * spread
+        if st["dtype"] == "bf16":
+            tol = tol + 2.0 ** -8 * np.abs(wo) + (0 if path == "simt" else 2.0 ** -8 * spread)
+        l_tol = s_err + 2.0 ** -23 * (64 + np.abs(wl)) * 4
+        assert (np.abs(l[b] - wl) <= l_tol).all(), (path, (np.abs(l[b] - wl) / l_tol).max())
+        assert (np.abs(o[b] - wo) <= tol + 1e-30).all(), (path, (np.abs(o[b] - wo) / (tol + 1e-30)).max())
+
+
+@pytest.mark.parametrize("q_scale", [1.0, 30.0])
+@pytest.mark.parametrize("P,Hq,H,D,k,ps,dtype", SHAPES, ids=lambda v: str(v).replace(" ", ""))
+def test_every_path_to_its_own_tolerance(P, Hq, H, D, k, ps, dtype, q_scale):
+    st = make(67 + len(P) + k, P, Hq, H, D, k, ps, dtype, q_scale=q_scale, stale="ff")
+    for path in paths(k, Hq // H, D, dtype):
+        compare_by_path(st, *run(st, path, append=False), path)
