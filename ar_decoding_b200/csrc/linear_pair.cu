@@ -33,6 +33,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -174,6 +175,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         if (ok) commit_pair(bar(BAR_ACC + buf), (uint16_t)3);
       }
     }
+    __syncwarp();                  // this warp releases the tensor memory below, together
   } else {
     // ---------------------------------------------------------------- epilogue
     const int q4 = warp & 3;       // TMEM lane quarter
@@ -204,20 +206,31 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         }
         if (f0 + c >= prm.N) continue;                     // warp-uniform
         if (prm.vec && f0 + c + 32 <= prm.N) {
-          if (row >= prm.T) continue;
-          __nv_bfloat16* dst = prm.y + at + c;
-          const __nv_bfloat16* res = prm.residual ? prm.residual + at + c : nullptr;
+          if (row < prm.T) {
+            __nv_bfloat16* dst = prm.y + at + c;
+            const __nv_bfloat16* res = prm.residual ? prm.residual + at + c : nullptr;
+            // one copy of the 32 values' code per activation, chosen once
+            auto write = [&](auto act) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            float b8[8], r8[8], v[8];
+              for (int e = 0; e < 32; e += 8) {
+                float b8[8], r8[8], v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) b8[i] = r8[i] = 0.f;
-            if (prm.bias) load_vec<__nv_bfloat16, 8>(prm.bias + f0 + c + e, b8);
-            if (res) load_vec<__nv_bfloat16, 8>(res + e, r8);
+                for (int i = 0; i < 8; ++i) b8[i] = r8[i] = 0.f;
+                if (prm.bias) load_vec<__nv_bfloat16, 8>(prm.bias + f0 + c + e, b8);
+                if (res) load_vec<__nv_bfloat16, 8>(res + e, r8);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = lin_act(__uint_as_float(acc[e + i]) + b8[i], prm.act) + r8[i];
-            *reinterpret_cast<uint4*>(dst + e) = make_uint4(tc05::cvt_bf16x2(v[0], v[1]), tc05::cvt_bf16x2(v[2], v[3]),
-                                                            tc05::cvt_bf16x2(v[4], v[5]), tc05::cvt_bf16x2(v[6], v[7]));
+                for (int i = 0; i < 8; ++i) v[i] = lin_act(__uint_as_float(acc[e + i]) + b8[i], decltype(act)::value) + r8[i];
+                *reinterpret_cast<uint4*>(dst + e) = make_uint4(tc05::cvt_bf16x2(v[0], v[1]), tc05::cvt_bf16x2(v[2], v[3]),
+                                                                tc05::cvt_bf16x2(v[4], v[5]), tc05::cvt_bf16x2(v[6], v[7]));
+              }
+            };
+            switch (prm.act) {
+              case TIDAR_ACT_RELU: write(std::integral_constant<int, TIDAR_ACT_RELU>{}); break;
+              case TIDAR_ACT_GELU: write(std::integral_constant<int, TIDAR_ACT_GELU>{}); break;
+              case TIDAR_ACT_GELU_TANH: write(std::integral_constant<int, TIDAR_ACT_GELU_TANH>{}); break;
+              case TIDAR_ACT_SILU: write(std::integral_constant<int, TIDAR_ACT_SILU>{}); break;
+              default: write(std::integral_constant<int, TIDAR_ACT_NONE>{});
+            }
           }
         } else {
           // a feature a lane, two rows an instruction: 32 contiguous bytes each (a
@@ -246,11 +259,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       }
     }
   }
-  // No MMA, copy or remote arrival is left when a CTA of the pair exits.
-  __syncwarp();                    // the roles parted the warps; the cluster barrier and the release want them whole
+  // No MMA, copy or remote arrival is left when a CTA of the pair exits.  (The producer's
+  // warp comes here in two parts; a __syncwarp behind its loop costs 1 % of the large
+  // products.)
   tc05::fence_before();
   __syncthreads();
-  cluster_sync_all();
+  cluster_sync_apart();
   if (warp == 1) {
     tc05::fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
