@@ -257,6 +257,15 @@ Plan make_plan(const tidar_step_desc* d, int path, bool kv4 = false) {
   return p;
 }
 
+// The family of a call.  AUTO over the 4-bit cache (bf16, D 128) takes DEC wherever it
+// has a form, up to 16 packed rows a head, then TC05; us of kernel for 32 sequences of
+// 512 to 16384 keys / one of 8192, by rows a head (q / KV heads, k):
+//   1 (8/8, 0)    DEC  76 / 10.3   TC05 242 / 18.7      16 (32/4, 1)  DEC 111 / 12.4   TC05 233 / 16.1
+//   4 (32/8, 0)   DEC  75 / 10.8   TC05 241 / 18.6      16 (16/1, 0)  DEC  36 / 12.0   TC05  69 / 17.6
+//   8 (32/8, 1)   DEC  78 / 11.6   TC05 242 / 18.8      20 (8/8, 4)   TC05 242 / 20.4   SIMT 15000 / 350
+//   12 (12/2, 1)  DEC  59 / 11.2   TC05 121 / 15.8      24 (32/8, 2)  TC05 242 / 20.4   SIMT 18000 / 420
+// From 17 rows on TC05 pays a whole tile's conversions for them: longer than the bf16
+// cache's step takes (179 / 15.5 at 20 rows).
 int choose_path(const tidar_step_desc* d, bool kv4 = false) {
   if (d->path == TIDAR_PATH_SIMT) return 1;
   if (d->path == TIDAR_PATH_TC05) return 2;

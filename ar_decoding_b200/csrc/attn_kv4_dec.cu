@@ -19,15 +19,21 @@
 //     word per group, each pair becomes 136 + c, minus 136, times the two keys'
 //     scales (exact in bf16; the sums run over the whole prefix here, so an
 //     offset in the accumulator would cost its low bits).
-// 32 sequences of 512 to 16384 keys, 8 KV heads: 77.5 us, 4.0 TB/s (0.61 of the copy
-// rate; the bf16 cache's kernel 168); one of 8192: 11.0 us in a cluster of ten splits.
+// 32 sequences of 512 to 16384 keys, 8 KV heads, 4 or 8 rows a head: 75 to 78 us, 4.0
+// TB/s (0.61 of the copy rate; the bf16 cache's kernel 164); one of 8192: 10.9 us in a
+// cluster of ten splits (bf16 9.6).  9 to 16 rows a head, two query tiles, whose registers
+// (255 a thread) leave eight warps: 16 rows, 4 KV heads 111 us, a third of one tile's
+// bytes a second (bf16 149, the tensor-core kernel 233); 12 rows, 2 KV heads 59 (80, 121).
 // No pipe is full (issue 60 %, integer 58 %, MMA 22 %; four warps a scheduler, whose
 // registers allow no more): a warp's chain of shifts, products and exponentials is
 // what a unit takes.  One multiply-add instead of subtract and multiply a value pair
 // made it no faster (82 us), nor did multiplies for shifts (104) or 20 warps of 96
 // registers (89).
-// Both products are exact up to the fp32 accumulation, so the only rounding
-// besides it is p's to bf16.  MMA row r of a 16-key block is physical key
+// Both products are exact up to the fp32 accumulation (the scores' partial sums reach
+// 143/7 of sum |q||k| by the offset, and round accordingly), so the only rounding besides
+// it is p's to bf16: an MMA's operands have one type, V's values are bf16, and the bf16
+// cache's step rounds p likewise (2^-8 of each p at most; p in two halves would double
+// the products).  MMA row r of a 16-key block is physical key
 // (r % 8) / 2 + 4 (r % 2) + 8 (r / 8): the four keys whose values a lane loads
 // are then t, t+4, t+8, t+12 and the loads of a warp cover 256 contiguous bytes.
 //

@@ -45,9 +45,11 @@
 // still come by TMA.  Rings of two stages make room for the raw rows.
 // Bound there: the bytes are 3.6 times fewer, but every tile of 128 packed rows
 // converts its blocks again, beside 16 softmax warps that want the same issue
-// slots.  32 q / 8 kv heads, 8192 keys, k = 16: 69.3 us (0.53 PFLOP/s; 55.3 over the
+// slots.  32 q / 8 kv heads, 8192 keys, k = 16: 69.2 us (0.53 PFLOP/s; 53.4 over the
 // bf16 cache; 57-63 without the conversions); 32 sequences of 512 to 16384 keys at
-// k = 8: 682 us (0.47 PFLOP/s; bf16 515, without the conversions 590).  Steps: seven
+// k = 8: 627 to 680 us by the box's power state (0.47 to 0.5 PFLOP/s; bf16 515 to 542,
+// without the conversions 590); at k = 2 and 4, one tile, 242 and 245 (bf16 179, 191).
+// p is rounded to bf16, V's type, as over the bf16 cache.  Steps: seven
 // converting warps that take a K and a V block in turn, in 24 warps of 80 registers
 // 85 / 838 us; eight in 28 warps of 72 82 / 765; the issuing thread without spilled
 // descriptors 75 / 732; the second softmax pass in two quarters 74 / 727; warps of
@@ -162,8 +164,8 @@ __device__ __forceinline__ void wait_ld32(uint32_t (&r)[32]) {
 }
 #undef TIDAR_RW8
 
-// 64 score columns: one TMEM load, or two of 32 columns where the launch's 80
-// registers a thread do not hold the wide one's operands (KV4).
+// 64 score columns: one TMEM load, or two of 32 columns where the softmax warps' 96
+// registers a thread do not hold the wide one's operands beside the rest (KV4).
 template <bool KV4>
 __device__ __forceinline__ void ld_half_row(uint32_t taddr, uint32_t (&x)[64]) {
   if constexpr (KV4) {

@@ -19,8 +19,8 @@
 // contiguous bytes a store group) runs under the MMAs of the next.  Rows, features
 // and the reduction may end anywhere: TMA reads zeros outside, stores are guarded.
 //
-// 2048 x 16384 x 4096, bias and tanh GELU: 191 us, 1.44 PFLOP/s (0.87 of the burst
-// rate of a library product; 224 us and 1.23 PFLOP/s in a loop of seconds under the
+// 2048 x 16384 x 4096, bias and tanh GELU: 191 to 201 us in a burst, 1.44 PFLOP/s (0.87 of
+// a library product's; 226 to 233 us and 1.2 PFLOP/s in a loop of seconds under the
 // power cap, where the library's product alone takes 215).  Without its loads the
 // loop takes 167 us: what is left is the 32 KB a slice and SM that come out of L2.
 // Tiles of 128 x 256 on single SMs took 454 us.  Eight epilogue warps: 1024 x 4096 x

@@ -21,7 +21,7 @@
 // and the reduction may end anywhere (TMA reads zeros outside).
 //
 // 272 x 4096 x 4096 with a residual: 16.9 us (0.54 PFLOP/s, 2.4 TB/s; the paired tiles
-// of linear_pair.cu 27); 1 x 16384 x 4096: 28.4 us, 4.7 TB/s; 77 x 1000 x 1544: 8.5 us,
+// of linear_pair.cu 27); 1 x 16384 x 4096: 28.4 us, 4.7 TB/s; 77 x 1000 x 1544: 7.7 to 11 us,
 // of which about 7 pass before the first product and after the last (launch,
 // cluster, TMEM, the first loads; the exchange of the partial sums).
 //

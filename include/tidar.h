@@ -539,9 +539,14 @@ tidar_status tidar_build_tables(const tidar_tables_desc* desc, const int32_t* pa
  *   TIDAR_PART_APPEND: the draft rows are quantised and stored); lse_out may be
  *   NULL with STEP_KEYS.  desc->dtype is that of q, k_blk, v_blk and out.
  *   Paths: AUTO; SIMT for every shape; for bf16 and head_dim 128, any page size,
- *   DEC (R * G <= 16) and TC05; PAIR is not offered.  A NaN among the values that a
- *   row attends makes the row's outputs NaN.  workspace as
- *   tidar_step_attn's, sized by tidar_step_attn_kv4_workspace_bytes.
+ *   DEC (R * G <= 16) and TC05; PAIR is not offered.  A NaN key makes the outputs
+ *   and the lse of every row that attends it NaN, as a NaN query does its own row's;
+ *   a NaN value makes its dims NaN there, whatever its weight and the splits.  A step
+ *   key that a row does not see has weight 0, and DEC and TC05 multiply v_blk by
+ *   that: a NaN or an infinity in v_blk may reach every row of its sequence and KV
+ *   head (one in k_blk reaches the rows that see it).  After BAD_PAGE or BAD_LEN
+ *   the sequence's outputs are unspecified.  workspace as tidar_step_attn's, sized
+ *   by tidar_step_attn_kv4_workspace_bytes.
  *   TIDAR_ERR_UNSUPPORTED when batch * num_kv_heads > 65535 or max_prefix_len >
  *   2^30 (this one for tidar_commit_kv4 too).
  * tidar_commit_kv4: tidar_commit over such a cache (rejected rows are zeroed).
