@@ -215,7 +215,11 @@ __global__ void __launch_bounds__(kWarps * 32) finalize_kernel(AttnArgs a, int m
     for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
     // KV4: the splits that saw a key.  Their rows count at a weight that came out as 0
     // too: 0 times a NaN value is NaN, as it is within a split.
-    const unsigned live_a = __ballot_sync(0xffffffffu, la != -INFINITY), live_b = __ballot_sync(0xffffffffu, lb != -INFINITY);
+    unsigned live_a = 0, live_b = 0;
+    if constexpr (KV4) {
+      live_a = __ballot_sync(0xffffffffu, la != -INFINITY);
+      live_b = __ballot_sync(0xffffffffu, lb != -INFINITY);
+    }
     float wa = 0.f, wb = 0.f, mx = -INFINITY, wsum = 0.f;
     for (int s0 = 0; s0 < ns; s0 += kFinChunk) {
       float v[kFinChunk][VPL];
